@@ -26,6 +26,8 @@ ERR_TIMEOUT = 6
 
 BF16 = 0
 FP32 = 1
+E4M3 = 0
+INT8 = 1
 ROLE_SPARSE = 0
 ROLE_RETRIEVAL = 1
 
@@ -37,13 +39,31 @@ EXPORTED = ("lychee_workspace_size", "lychee_layer_workspace_size", "lychee_work
             "lychee_check_device_error", "lychee_status_string", "lychee_version",
             "lychee_profile_begin", "lychee_profile_spans_begin", "lychee_profile_end",
             "lychee_append_kv",
-            "lychee_hardkuma_roles", "lychee_hybrid_decode_attn_swa", "lychee_decode_stack_swa")
+            "lychee_hardkuma_roles", "lychee_hybrid_decode_attn_swa", "lychee_decode_stack_swa",
+            "lychee_append_rope_q8", "lychee_q8_workspace_size", "lychee_decode_attn_q8",
+            "lychee_hybrid_decode_attn_q8")
 
 
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("N_max", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("k", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class Q8Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "Hq", "Hkv", "d", "page", "num_pages", "max_pages", "dtype", "code")]
+
+
+class Q8CachePtrs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table")]
+
+
+class Q8Tokens(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out")] +
+                [(n, ctypes.c_int64) for n in ("k_stride", "v_stride", "q_stride")] +
+                [(n, ctypes.c_void_p) for n in ("cos_sin", "cu_new")] +
+                [(n, ctypes.c_int32) for n in ("T", "n_pos", "rot", "interleaved")])
 
 
 class LycheeError(RuntimeError):
@@ -94,6 +114,16 @@ def load(path: str | None = None):
         lib.lychee_hardkuma_roles.argtypes = [vp, vp, i32, i32, ctypes.c_double, ctypes.c_double,
                                               i32, vp, vp, vp, vp]
         lib.lychee_hardkuma_roles.restype = ctypes.c_int
+        qp, cp = ctypes.POINTER(Q8Shape), ctypes.POINTER(Q8CachePtrs)
+        lib.lychee_append_rope_q8.argtypes = [qp, cp, ctypes.POINTER(Q8Tokens), vp, vp, vp]
+        lib.lychee_append_rope_q8.restype = ctypes.c_int
+        lib.lychee_q8_workspace_size.argtypes = [qp, i32]
+        lib.lychee_q8_workspace_size.restype = ctypes.c_size_t
+        lib.lychee_decode_attn_q8.argtypes = [qp, vp, cp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+        lib.lychee_decode_attn_q8.restype = ctypes.c_int
+        lib.lychee_hybrid_decode_attn_q8.argtypes = [qp, i32, i32, vp, cp] + [vp] * 7 + [
+            ctypes.c_size_t, vp, vp]
+        lib.lychee_hybrid_decode_attn_q8.restype = ctypes.c_int
         lib.lychee_check_device_error.argtypes = [vp, vp, u32p]
         lib.lychee_check_device_error.restype = ctypes.c_int
         lib.lychee_status_string.argtypes = [ctypes.c_int]

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "blocksel.h"
+#include "host.h"
 #include "kernels.h"
 #include "lychee.h"
 
@@ -34,8 +35,6 @@ struct Layout {
   size_t bitmaps, layer_total, total;
   int nchunk, nwords;
 };
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The shortest attention work item the shape may get: kChunkMin positions, or
 // kChunkSmall when the layer's K/V rows (B * Hkv * N_max) are too few to give
@@ -99,37 +98,7 @@ Layout layout_of(const lychee_shape* s) {
   return L;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 size_t elem_size(const lychee_shape* s) { return s->dtype == LYCHEE_BF16 ? 2 : 4; }
-
-lychee_status check_roles(const uint8_t* role, int Hq, int* n_sparse) {
-  if (!role) return LYCHEE_ERR_INVALID_ARG;
-  int ns = 0;
-  for (int h = 0; h < Hq; ++h) {
-    if (role[h] != LYCHEE_ROLE_SPARSE && role[h] != LYCHEE_ROLE_RETRIEVAL)
-      return LYCHEE_ERR_INVALID_ARG;
-    ns += role[h] == LYCHEE_ROLE_SPARSE;
-  }
-  if (n_sparse) *n_sparse = ns;
-  return LYCHEE_OK;
-}
-
-// ---- device properties -----------------------------------------------------------
-int num_sms_current() {
-  static std::mutex mu;
-  static std::vector<int> cache;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  std::lock_guard<std::mutex> g(mu);
-  if ((int)cache.size() <= dev) cache.resize(dev + 1, 0);
-  if (cache[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
 
 // ---- tensor maps for the attention kernel's row gathers -----------------------------
 // cuTensorMapEncodeTiled comes from the driver through the runtime's entry-point
@@ -219,67 +188,6 @@ bool encode_tile_map(CUtensorMap* m, const void* base, const lychee_shape* s, in
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// ---- optional launch profiler ----------------------------------------------------
-// Per-launch mode: two events around every launch.  Span mode: two events per
-// stack call, before its first attention launch and after its last one, and
-// none in between, so that the layers still overlap.
-struct Profiler {
-  std::mutex mu;
-  bool on = false;
-  bool spans = false;
-  int cap = 0, n = 0;
-  std::vector<cudaEvent_t> ev;
-  std::vector<int32_t> kinds;
-};
-Profiler g_prof;
-
-enum {
-  kKindAttn = 0,
-  kKindTopk = 1,
-  kKindCombine = 2,
-  kKindBuildBits = 3,
-  kKindExport = 4,
-  kKindTopkCombine = 5,
-  kKindAttnSpan = 6
-};
-
-// Span mode: open (end = false) or close (end = true) the current stack call's
-// attention span on `st`.
-void span_mark(bool end, cudaStream_t st) {
-  if (!g_prof.on || !g_prof.spans) return;
-  std::lock_guard<std::mutex> g(g_prof.mu);
-  if (!g_prof.on || !g_prof.spans) return;
-  if (!end) {
-    if (g_prof.n >= g_prof.cap) return;
-    const int i = g_prof.n++;
-    g_prof.kinds[i] = -1;   // open
-    cudaEventRecord(g_prof.ev[2 * i], st);
-  } else if (g_prof.n > 0 && g_prof.kinds[g_prof.n - 1] == -1) {
-    const int i = g_prof.n - 1;
-    g_prof.kinds[i] = kKindAttnSpan;
-    cudaEventRecord(g_prof.ev[2 * i + 1], st);
-  }
-}
-
-template <typename F>
-cudaError_t timed(int kind, cudaStream_t st, F&& launch) {
-  if (!g_prof.on || g_prof.spans) return launch();
-  std::lock_guard<std::mutex> g(g_prof.mu);
-  if (!g_prof.on || g_prof.spans || g_prof.n >= g_prof.cap) return launch();
-  const int i = g_prof.n++;
-  g_prof.kinds[i] = kind;
-  cudaEventRecord(g_prof.ev[2 * i], st);
-  const cudaError_t e = launch();
-  cudaEventRecord(g_prof.ev[2 * i + 1], st);
-  return e;
-}
-
-void fill_roles(uint32_t (&bits)[4], const uint8_t* role, int Hq) {
-  bits[0] = bits[1] = bits[2] = bits[3] = 0;
-  for (int h = 0; h < Hq; ++h)
-    if (role[h] == LYCHEE_ROLE_RETRIEVAL) bits[h >> 5] |= 1u << (h & 31);
 }
 
 struct Ctx {

@@ -209,16 +209,18 @@ __device__ __forceinline__ void block_select_body(const BlockSelParams& p, int p
   }
   if (p.idx_out) {
     int32_t* orow = p.idx_out + bh * p.k;
+    // entries of the index row the set may fill (none for an empty sequence)
+    const int row_cap = p.empty_ok && p.seqlens[b] <= 0 ? 0 : p.k;
     for (int c = warp; c < nblk; c += kSelWarps) {
       const uint32_t off = keys[c];
       if (off == kFull) continue;
       const int j0 = c * block, len = min(block, n - j0);
       for (int i = lane; i < len; i += 32)
-        if (off + i < (uint32_t)p.k) orow[off + i] = j0 + i;
+        if (off + i < (uint32_t)row_cap) orow[off + i] = j0 + i;
     }
     // positions in the set: whole blocks, the tail block (if taken) cut at n_b
     const int m = (int)sel_seen * block - (keys[nblk - 1] != kFull ? nblk * block - n : 0);
-    for (int t = m + tid; t < p.k; t += kSelThreads) orow[t] = -1;
+    for (int t = min(m, row_cap) + tid; t < p.k; t += kSelThreads) orow[t] = -1;
   }
   cluster_wait();
 }

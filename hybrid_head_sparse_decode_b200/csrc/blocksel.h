@@ -17,6 +17,7 @@ struct BlockSelParams {
   int32_t* idx_out;          // [B, Hq, k] or null: ascending, -1 padded
   uint32_t* err;
   int B, Hq, N_max, nwords, k, nheads, block;
+  int empty_ok;              // 1: a sequence of no rows gets an empty set (0: n_b counts as 1)
   uint8_t heads[128];        // the retrieval heads handled by this launch
 };
 // block keys of one head, at most 32768 blocks (see block_select_smem)

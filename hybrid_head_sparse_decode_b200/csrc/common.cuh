@@ -21,6 +21,7 @@ enum : uint32_t {
   kErrBadSeqlen = 2u,   // n_b outside [1, N_max] (clamped)
   kErrBadBudget = 4u,   // k_per_seq[b] < 1 (clamped to 1)
   kErrTimeout = 8u,     // a pipeline wait gave up
+  kErrNotFinite = 16u,  // the 8-bit append met a value that is not finite
 };
 
 // Workspace header: 256 bytes at offset 0.

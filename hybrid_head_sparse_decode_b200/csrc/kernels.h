@@ -85,6 +85,7 @@ struct TopkParams {
   uint32_t* err;
   int B, Hq, N_max, nwords, k, nheads;
   int sms;                   // SMs of the device (the cluster size is picked by waves)
+  int empty_ok;              // 1: a sequence of no rows gets an empty set (0: n_b counts as 1)
   uint8_t heads[128];        // the retrieval heads handled by this launch
 };
 

@@ -1,0 +1,53 @@
+// q8.h -- parameter blocks and launchers of the 8-bit paged cache's kernels (internal).
+#pragma once
+
+#include "kernels.h"
+
+namespace lychee {
+
+// The cache of one layer: codes [num_pages, Hkv, page, D] of 8 bits, one fp32
+// scale per page and head, and the pages of each sequence.
+struct Q8Cache {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;      // [num_pages, Hkv]
+  const float* v_scale;
+  const int32_t* table;      // [B, max_pages]: page of positions [j * page, (j + 1) * page)
+  int num_pages, max_pages;
+  int page_log2;             // page = 1 << page_log2 positions (16 .. 128)
+};
+
+// New rows into the cache, rotated and quantised; queries rotated (q8_append.cu).
+struct Q8AppendParams {
+  Q8Cache c;                 // written: k, v, k_scale, v_scale
+  const void* k_new;         // [T, Hkv, D], rows of one token k_stride elements apart
+  const void* v_new;
+  const void* q;             // [T, Hq, D] or null
+  void* q_out;               // [T, Hq, D]
+  long long k_stride, v_stride, q_stride;   // elements from one token to the next
+  const float* cos_sin;      // [n_pos, rot]: cosines, then sines; null: no rotation
+  const int32_t* cu_new;     // [B + 1] or null: one token a sequence
+  const int32_t* seqlens;    // [B], the new tokens included
+  uint32_t* err;             // or null
+  int B, T, Hq, Hkv, n_pos, rot, interleaved;
+};
+cudaError_t launch_q8_append(const Q8AppendParams& p, int dtype, int code, int D, cudaStream_t st);
+
+// Attention of one query token a sequence over the cache (q8_attn.cu).
+struct Q8AttnParams {
+  Q8Cache c;
+  const void* q;             // [B, Hq, D]
+  void* out;                 // [B, Hq, D]
+  const int32_t* seqlens;    // [B]
+  const int32_t* idx_in;     // [B, Hq, k] or null: sets of the sparse heads
+  int32_t* idx_out;          // [B, Hq, k] or null
+  float* logits;             // [B, Hq, N_max] or null: raw q.k of the retrieval heads
+  uint32_t* err;
+  int B, Hq, Hkv, N_max, k;
+  float scale_log2;          // log2(e) / sqrt(D)
+  uint32_t role[4];          // bit h set: head h attends to every position
+};
+cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms,
+                           cudaStream_t st);
+
+}  // namespace lychee

@@ -1,0 +1,227 @@
+// q8_api.cu -- the C ABI of the 8-bit paged cache (declared in include/lychee.h):
+// argument checks, workspace layout and launches.  Host code only; no memory is
+// allocated here.
+#include <cmath>
+#include <cstring>
+
+#include "blocksel.h"
+#include "common.cuh"
+#include "host.h"
+#include "lychee.h"
+#include "q8.h"
+
+using namespace lychee;
+
+namespace {
+
+bool pow2_page(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+lychee_status check_q8_shape(const lychee_q8_shape* s) {
+  if (!s) return LYCHEE_ERR_INVALID_ARG;
+  if (s->B < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1 || s->num_pages < 1 || s->max_pages < 1 || s->page < 1)
+    return LYCHEE_ERR_INVALID_ARG;
+  if (s->dtype != LYCHEE_BF16 && s->dtype != LYCHEE_FP32) return LYCHEE_ERR_INVALID_ARG;
+  if (s->code != LYCHEE_E4M3 && s->code != LYCHEE_INT8) return LYCHEE_ERR_INVALID_ARG;
+  if (s->Hq % s->Hkv != 0) return LYCHEE_ERR_INVALID_ARG;
+  const int G = s->Hq / s->Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return LYCHEE_ERR_UNSUPPORTED;
+  if (s->Hq > kMaxHq || (s->d != 64 && s->d != 128) || !pow2_page(s->page)) return LYCHEE_ERR_UNSUPPORTED;
+  if ((long long)s->max_pages * s->page > (1 << 24)) return LYCHEE_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits
+  if ((long long)s->num_pages * s->Hkv * s->page > 0x7fffffffLL) return LYCHEE_ERR_UNSUPPORTED;
+  if ((long long)s->B * s->Hq >= (1LL << 24)) return LYCHEE_ERR_UNSUPPORTED;
+  return LYCHEE_OK;
+}
+
+lychee_status check_q8_cache(const lychee_q8_cache* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table) return LYCHEE_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(c->block_table, 4))
+    return LYCHEE_ERR_INVALID_ARG;
+  return LYCHEE_OK;
+}
+
+Q8Cache cache_of(const lychee_q8_shape* s, const lychee_q8_cache* c) {
+  Q8Cache r{};
+  r.k = static_cast<const uint8_t*>(c->k);
+  r.v = static_cast<const uint8_t*>(c->v);
+  r.k_scale = c->k_scale;
+  r.v_scale = c->v_scale;
+  r.table = c->block_table;
+  r.num_pages = s->num_pages;
+  r.max_pages = s->max_pages;
+  while ((1 << r.page_log2) < s->page) ++r.page_log2;
+  return r;
+}
+
+int n_max_of(const lychee_q8_shape* s) { return s->max_pages * s->page; }
+
+// Workspace: for the hybrid step (k > 0), the retrieval heads' logits.
+struct Q8Layout {
+  size_t logits, total;
+};
+Q8Layout q8_layout(const lychee_q8_shape* s, int k) {
+  Q8Layout L{};
+  L.logits = 0;
+  L.total = 256 + (k > 0 ? align256((size_t)s->B * s->Hq * n_max_of(s) * 4) : 0);
+  return L;
+}
+
+lychee_status check_sets(const lychee_q8_shape* s, int k, int block) {
+  const int n_max = n_max_of(s);
+  if (k < 1 || k > n_max || block < 0) return LYCHEE_ERR_INVALID_ARG;
+  if (block > 1) {
+    if (block % 32 != 0 || block > 1024 || block > k) return LYCHEE_ERR_INVALID_ARG;
+    if (block_select_smem(n_max, block) > kBlockSelSmemMax) return LYCHEE_ERR_UNSUPPORTED;
+  }
+  return LYCHEE_OK;
+}
+
+Q8AttnParams attn_params(const lychee_q8_shape* s, const void* q, const lychee_q8_cache* c,
+                         const int32_t* seqlens, void* out, uint32_t* err) {
+  Q8AttnParams p{};
+  p.c = cache_of(s, c);
+  p.q = q;
+  p.out = out;
+  p.seqlens = seqlens;
+  p.err = err;
+  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv;
+  p.N_max = n_max_of(s);
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s->d));
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k) {
+  if (check_q8_shape(s) != LYCHEE_OK || k < 0 || k > n_max_of(s)) return 0;
+  return q8_layout(s, k).total;
+}
+
+lychee_status lychee_append_rope_q8(const lychee_q8_shape* s, const lychee_q8_cache* cache,
+                                    const lychee_q8_tokens* t, const int32_t* seqlens,
+                                    uint32_t* device_error, void* stream) {
+  lychee_status st = check_q8_shape(s);
+  if (st != LYCHEE_OK) return st;
+  if ((st = check_q8_cache(cache)) != LYCHEE_OK) return st;
+  if (!t || !t->k || !t->v || !seqlens || t->T < 0) return LYCHEE_ERR_INVALID_ARG;
+  if ((t->q != nullptr) != (t->q_out != nullptr)) return LYCHEE_ERR_INVALID_ARG;
+  if (!t->cu_new && t->T != s->B) return LYCHEE_ERR_INVALID_ARG;
+  const int es = s->dtype == LYCHEE_BF16 ? 2 : 4;
+  auto row_ok = [&](const void* p, int64_t stride, int heads) {
+    return aligned(p, 16) && stride >= (int64_t)heads * s->d && stride * es % 16 == 0;
+  };
+  if (!row_ok(t->k, t->k_stride, s->Hkv) || !row_ok(t->v, t->v_stride, s->Hkv)) return LYCHEE_ERR_INVALID_ARG;
+  if (t->q && (!row_ok(t->q, t->q_stride, s->Hq) || !aligned(t->q_out, 16))) return LYCHEE_ERR_INVALID_ARG;
+  if (t->cos_sin && (t->rot < 8 || t->rot > s->d || t->rot % 8 != 0 || t->n_pos < 1 || !aligned(t->cos_sin, 16)))
+    return LYCHEE_ERR_INVALID_ARG;
+  if (!aligned(t->cu_new, 4) || !aligned(seqlens, 4) || !aligned(device_error, 4)) return LYCHEE_ERR_INVALID_ARG;
+  Q8AppendParams p{};
+  p.c = cache_of(s, cache);
+  p.k_new = t->k;
+  p.v_new = t->v;
+  p.q = t->q;
+  p.q_out = t->q_out;
+  p.k_stride = t->k_stride;
+  p.v_stride = t->v_stride;
+  p.q_stride = t->q_stride;
+  p.cos_sin = t->cos_sin;
+  p.cu_new = t->cu_new;
+  p.seqlens = seqlens;
+  p.err = device_error;
+  p.B = s->B; p.T = t->T; p.Hq = s->Hq; p.Hkv = s->Hkv;
+  p.n_pos = t->n_pos;
+  p.rot = t->cos_sin ? t->rot : 0;
+  p.interleaved = t->interleaved ? 1 : 0;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      timed(kKindAppend, cs, [&] { return launch_q8_append(p, s->dtype, s->code, s->d, cs); });
+  return e == cudaSuccess ? LYCHEE_OK : LYCHEE_ERR_CUDA;
+}
+
+lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q, const lychee_q8_cache* cache,
+                                    const int32_t* seqlens, void* out, void* workspace,
+                                    size_t workspace_bytes, uint32_t* device_error, void* stream) {
+  lychee_status st = check_q8_shape(s);
+  if (st != LYCHEE_OK) return st;
+  if ((st = check_q8_cache(cache)) != LYCHEE_OK) return st;
+  if (!q || !seqlens || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(seqlens, 4) ||
+      !aligned(device_error, 4))
+    return LYCHEE_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < q8_layout(s, 0).total || !aligned(workspace, 256))
+    return LYCHEE_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return LYCHEE_ERR_CUDA;
+  Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error);
+  for (int i = 0; i < 4; ++i) p.role[i] = 0xffffffffu;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); });
+  return e == cudaSuccess ? LYCHEE_OK : LYCHEE_ERR_CUDA;
+}
+
+lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, int32_t block, const void* q,
+                                           const lychee_q8_cache* cache, const int32_t* seqlens,
+                                           const int32_t* k_per_seq, const uint8_t* head_role,
+                                           const int32_t* idx_in, void* out, int32_t* idx_out,
+                                           void* workspace, size_t workspace_bytes, uint32_t* device_error, void* stream) {
+  lychee_status st = check_q8_shape(s);
+  if (st != LYCHEE_OK) return st;
+  if ((st = check_q8_cache(cache)) != LYCHEE_OK) return st;
+  if ((st = check_sets(s, k, block)) != LYCHEE_OK) return st;
+  int ns = 0;
+  if ((st = check_roles(head_role, s->Hq, &ns)) != LYCHEE_OK) return st;
+  if (!q || !seqlens || !out || !idx_out || (ns > 0 && !idx_in)) return LYCHEE_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seqlens, 4) || !aligned(k_per_seq, 4) ||
+      !aligned(idx_in, 4) || !aligned(idx_out, 4) || !aligned(device_error, 4))
+    return LYCHEE_ERR_INVALID_ARG;
+  const Q8Layout L = q8_layout(s, k);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return LYCHEE_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return LYCHEE_ERR_CUDA;
+  Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error);
+  p.idx_in = idx_in;
+  p.idx_out = idx_out;
+  p.k = k;
+  p.logits = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.logits);
+  fill_roles(p.role, head_role, s->Hq);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); }) != cudaSuccess)
+    return LYCHEE_ERR_CUDA;
+  if (ns == s->Hq) return LYCHEE_OK;
+  // the retrieval heads' selection, as over any cache
+  TopkParams tp{};
+  tp.logits = p.logits;
+  tp.seqlens = seqlens;
+  tp.k_per_seq = k_per_seq;
+  tp.idx_out = idx_out;
+  tp.err = p.err;
+  tp.B = s->B; tp.Hq = s->Hq; tp.N_max = p.N_max; tp.nwords = (p.N_max + 31) / 32; tp.k = k;
+  tp.sms = sms;
+  tp.empty_ok = 1;
+  for (int h = 0; h < s->Hq; ++h)
+    if (head_role[h] == LYCHEE_ROLE_RETRIEVAL) tp.heads[tp.nheads++] = (uint8_t)h;
+  CombineParams none{};   // B = 0: selection only
+  cudaError_t e;
+  if (block > 1) {
+    BlockSelParams bp{};
+    bp.logits = tp.logits;
+    bp.seqlens = seqlens;
+    bp.k_per_seq = k_per_seq;
+    bp.idx_out = idx_out;
+    bp.err = tp.err;
+    bp.B = tp.B; bp.Hq = tp.Hq; bp.N_max = tp.N_max; bp.nwords = tp.nwords; bp.k = k;
+    bp.nheads = tp.nheads;
+    bp.block = block;
+    bp.empty_ok = 1;
+    std::memcpy(bp.heads, tp.heads, sizeof(bp.heads));
+    e = timed(kKindTopk, cs, [&] { return launch_block_select_combine(bp, none, s->dtype, s->d, cs); });
+  } else {
+    e = timed(kKindTopk, cs, [&] { return launch_topk_combine(tp, none, s->dtype, s->d, cs); });
+  }
+  return e == cudaSuccess ? LYCHEE_OK : LYCHEE_ERR_CUDA;
+}
+
+}  // extern "C"

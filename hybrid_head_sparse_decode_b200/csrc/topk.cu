@@ -135,6 +135,8 @@ __device__ __forceinline__ void topk_body(const TopkParams& p, int keys_cap, int
   const int n = min(max(p.seqlens[b], 1), p.N_max);
   int kb = p.k_per_seq ? p.k_per_seq[b] : p.k;
   kb = min(min(max(kb, 1), p.k), n);
+  // entries of the index row the set may fill (none for an empty sequence)
+  const int row_cap = p.empty_ok && p.seqlens[b] <= 0 ? 0 : p.k;
   const int words = (n + 31) >> 5;
   const int wpc = (words + C - 1) / C;
   const int w0 = min(words, (int)rank * wpc), w1 = min(words, w0 + wpc);
@@ -314,7 +316,7 @@ __device__ __forceinline__ void topk_body(const TopkParams& p, int keys_cap, int
         const uint32_t o2 = __shfl_sync(kFull, off, t);
         if ((s2 >> lane) & 1u) {
           const uint32_t o = o2 + __popc(s2 & ((1u << lane) - 1u));
-          if (o < (uint32_t)p.k) orow[o] = pos0 + (g0 + t) * 32 + lane;
+          if (o < (uint32_t)row_cap) orow[o] = pos0 + (g0 + t) * 32 + lane;
         }
       }
     }
@@ -322,7 +324,7 @@ __device__ __forceinline__ void topk_body(const TopkParams& p, int keys_cap, int
     run_sel += __shfl_sync(kFull, is, 31);
   }
   if (orow)
-    for (int t = kb + (int)rank * kThreads + tid; t < p.k; t += C * kThreads) orow[t] = -1;
+    for (int t = min(kb, row_cap) + (int)rank * kThreads + tid; t < p.k; t += C * kThreads) orow[t] = -1;
   cluster_wait();    // no CTA leaves while a histogram may still be on its way to it
 }
 

@@ -13,12 +13,14 @@ them, and hands raw pointers to the library on the current (or given) stream.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
 from . import _native as N
 
 _DT = {torch.bfloat16: N.BF16, torch.float32: N.FP32}
+_CODE = {torch.float8_e4m3fn: N.E4M3, torch.int8: N.INT8}
 
 
 def _ptr(t):
@@ -293,6 +295,231 @@ def append_kv(k_new, v_new, k_cache, v_cache, seqlens, stream=None):
     return k_cache, v_cache
 
 
+class Q8Cache(NamedTuple):
+    """One layer's 8-bit paged cache.  k, v: codes [num_pages, Hkv, page, d] (torch.float8_e4m3fn
+    or torch.int8); k_scale, v_scale [num_pages, Hkv] fp32: a page's rows of one head hold
+    code * scale."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def alloc_q8_cache(num_pages, Hkv, page, d, code=torch.float8_e4m3fn, device=None) -> Q8Cache:
+    """An uninitialised cache (a page is written before it is read)."""
+    if code not in _CODE:
+        raise TypeError(f"code must be torch.float8_e4m3fn or torch.int8, got {code}")
+    dev = device or "cuda"
+    k, v = (torch.empty((num_pages, Hkv, page, d), dtype=code, device=dev) for _ in range(2))
+    ks, vs = (torch.ones((num_pages, Hkv), dtype=torch.float32, device=dev) for _ in range(2))
+    return Q8Cache(k, v, ks, vs)
+
+
+def make_q8_shape(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code) -> N.Q8Shape:
+    return N.Q8Shape(int(B), int(Hq), int(Hkv), int(d), int(page), int(num_pages), int(max_pages),
+                     int(_DT.get(dtype, dtype)), int(_CODE.get(code, code)))
+
+
+def q8_workspace_size(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k=0) -> int:
+    """Bytes of workspace of decode_attn_q8 (k = 0) or of hybrid_decode_attn_q8 with sets of
+    capacity k."""
+    sh = make_q8_shape(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code)
+    n = N.load().lychee_q8_workspace_size(ctypes.byref(sh), int(k))
+    if n == 0:
+        raise N.LycheeError(N.ERR_INVALID_ARG, "q8_workspace_size")
+    return int(n)
+
+
+def alloc_q8_workspace(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k=0,
+                       device=None) -> torch.Tensor:
+    n = q8_workspace_size(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev):
+    """The checked cache of a call: its shape and pointers for the library."""
+    if not isinstance(cache, Q8Cache):
+        raise TypeError("cache must be a Q8Cache")
+    _need_cuda("cache.k", cache.k, device=dev)
+    if cache.k.dtype not in _CODE:
+        raise TypeError(f"cache.k must be torch.float8_e4m3fn or torch.int8, got {cache.k.dtype}")
+    if cache.k.dim() != 4 or cache.k.shape[3] != d:
+        raise ValueError(f"cache.k must be [num_pages, Hkv, page, {d}], got {tuple(cache.k.shape)}")
+    P, Hkv, page, _ = cache.k.shape
+    _need_cuda("cache.v", cache.v, cache.k.dtype, (P, Hkv, page, d), device=dev)
+    _need_cuda("cache.k_scale", cache.k_scale, torch.float32, (P, Hkv), device=dev)
+    _need_cuda("cache.v_scale", cache.v_scale, torch.float32, (P, Hkv), device=dev)
+    _need_cuda("block_table", block_table, torch.int32, device=dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    _need_cuda("seqlens", seqlens, torch.int32, (B,), device=dev)
+    sh = make_q8_shape(B, Hq, Hkv, d, page, P, max_pages, dt, cache.k.dtype)
+    ptrs = N.Q8CachePtrs(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                         cache.v_scale.data_ptr(), block_table.data_ptr())
+    return sh, ptrs
+
+
+def _need_rows(name, t, dt, shape, dev):
+    """Rows [T, heads, d] of dtype dt whose tokens may lie further apart than a row's end (a part
+    of a projection's output).  Returns the elements from one token to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, but the call runs on {dev}")
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, heads, d = shape
+    ok = t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)
+    stride = t.stride(0) if T > 1 else heads * d
+    if not ok or stride < heads * d:
+        raise ValueError(f"{name}: the rows of one token must be contiguous")
+    if stride * t.element_size() % 16 != 0 or t.data_ptr() % 16 != 0:
+        raise ValueError(f"{name}: tokens must begin on 16-byte boundaries")
+    return stride
+
+
+def _need_error(device_error, dev):
+    if device_error is not None:
+        _need_cuda("device_error", device_error, torch.int32, (1,), device=dev)
+
+
+def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q=None, cu_new=None,
+                   interleaved=False, q_out=None, device_error=None, stream=None):
+    """New keys and values [T, Hkv, d] (bf16 or fp32) into the 8-bit paged cache, in place, rotated
+    by their positions on the way; the queries q [T, Hq, d] (or None) rotated beside them.
+
+    cu_new [B + 1] int32: sequence b's tokens are cu_new[b] .. cu_new[b + 1] - 1 (None: token b).
+    seqlens [B] int32 counts the new tokens.  cos_sin [n_pos, rot] fp32: cosines, then sines, of
+    every position's rot / 2 angles (None: no rotation); interleaved: pairs (2i, 2i + 1) instead of
+    (i, i + rot / 2).  Rows of k_new, v_new and q may be parts of one projection output.
+    Returns the rotated queries [T, Hq, d], or None without q."""
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+        raise ValueError("k_new must be a tensor [T, Hkv, d]")
+    T, Hkv, d = k_new.shape
+    dt, dev = k_new.dtype, k_new.device
+    if dt not in _DT:
+        raise TypeError(f"k_new must be torch.bfloat16 or torch.float32, got {dt}")
+    ks = _need_rows("k_new", k_new, dt, (T, Hkv, d), dev)
+    vs = _need_rows("v_new", v_new, dt, (T, Hkv, d), dev)
+    Hq, qs = Hkv, 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a tensor [T, Hq, d]")
+        Hq = q.shape[1]
+        qs = _need_rows("q", q, dt, (T, Hq, d), dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+        _need_cuda("q_out", q_out, dt, (T, Hq, d), device=dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    sh, ptrs = _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev)
+    if cache.k.shape[1] != Hkv:
+        raise ValueError(f"k_new has {Hkv} heads, the cache {cache.k.shape[1]}")
+    if cu_new is not None:
+        _need_cuda("cu_new", cu_new, torch.int32, (sh.B + 1,), device=dev)
+    elif T != sh.B:
+        raise ValueError(f"without cu_new there is one token a sequence: got {T} for {sh.B}")
+    n_pos = rot = 0
+    if cos_sin is not None:
+        _need_cuda("cos_sin", cos_sin, torch.float32, device=dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [n_pos, rot]")
+        n_pos, rot = cos_sin.shape
+    _need_error(device_error, dev)
+    if T == 0:
+        return q_out
+    tok = N.Q8Tokens(k_new.data_ptr(), v_new.data_ptr(), None if q is None else q.data_ptr(),
+                     None if q is None else q_out.data_ptr(), ks, vs, qs,
+                     None if cos_sin is None else cos_sin.data_ptr(),
+                     None if cu_new is None else cu_new.data_ptr(), T, n_pos, rot,
+                     int(bool(interleaved)))
+    with torch.cuda.device(dev):
+        st = N.load().lychee_append_rope_q8(ctypes.byref(sh), ctypes.byref(ptrs), ctypes.byref(tok),
+                                            _ptr(seqlens), _ptr(device_error),
+                                            _stream_handle(stream, dev))
+    _check(st, "lychee_append_rope_q8")
+    return q_out
+
+
+def _q8_query(q, out):
+    _need_cuda("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    if q.dtype not in _DT:
+        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
+    if out is None:
+        out = torch.empty_like(q)
+    _need_cuda("out", out, q.dtype, tuple(q.shape), device=q.device)
+    return out
+
+
+def _q8_workspace(workspace, sh, k, dev):
+    if workspace is None:
+        n = N.load().lychee_q8_workspace_size(ctypes.byref(sh), int(k))
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _need_cuda("workspace", workspace, torch.uint8, device=dev)
+    return workspace
+
+
+def decode_attn_q8(q, cache, block_table, seqlens, *, out=None, workspace=None, device_error=None,
+                   stream=None):
+    """Attention of one query token a sequence over every position of the 8-bit paged cache.
+    q [B, Hq, d] (bf16 or fp32), block_table [B, max_pages] int32, seqlens [B] int32.
+    Returns out [B, Hq, d]."""
+    out = _q8_query(q, out)
+    B, Hq, d = q.shape
+    dev = q.device
+    sh, ptrs = _q8_cache(cache, block_table, seqlens, Hq, d, q.dtype, dev)
+    if sh.B != B:
+        raise ValueError(f"q has {B} sequences, block_table {sh.B}")
+    _need_error(device_error, dev)
+    workspace = _q8_workspace(workspace, sh, 0, dev)
+    with torch.cuda.device(dev):
+        st = N.load().lychee_decode_attn_q8(ctypes.byref(sh), _ptr(q), ctypes.byref(ptrs),
+                                            _ptr(seqlens), _ptr(out), _ptr(workspace),
+                                            ctypes.c_size_t(workspace.numel()), _ptr(device_error),
+                                            _stream_handle(stream, dev))
+    _check(st, "lychee_decode_attn_q8")
+    return out
+
+
+def hybrid_decode_attn_q8(q, cache, block_table, seqlens, head_role, idx_in, k, *, k_per_seq=None,
+                          out=None, idx_out=None, workspace=None, device_error=None, stream=None,
+                          block=0):
+    """hybrid_decode_attn over the 8-bit paged cache: one hybrid-head layer.  q, head_role, idx_in,
+    k, k_per_seq and block as there; cache, block_table and seqlens as in decode_attn_q8.
+    Returns (out [B, Hq, d], idx_out [B, Hq, k])."""
+    out = _q8_query(q, out)
+    B, Hq, d = q.shape
+    dev = q.device
+    sh, ptrs = _q8_cache(cache, block_table, seqlens, Hq, d, q.dtype, dev)
+    if sh.B != B:
+        raise ValueError(f"q has {B} sequences, block_table {sh.B}")
+    if k_per_seq is not None:
+        _need_cuda("k_per_seq", k_per_seq, torch.int32, (B,), device=dev)
+    if idx_in is not None:
+        _need_cuda("idx_in", idx_in, torch.int32, (B, Hq, k), device=dev)
+    role = _roles_host(head_role, Hq)
+    if idx_out is None:
+        idx_out = torch.empty((B, Hq, k), dtype=torch.int32, device=dev)
+    _need_cuda("idx_out", idx_out, torch.int32, (B, Hq, k), device=dev)
+    _need_error(device_error, dev)
+    workspace = _q8_workspace(workspace, sh, k, dev)
+    with torch.cuda.device(dev):
+        st = N.load().lychee_hybrid_decode_attn_q8(
+            ctypes.byref(sh), ctypes.c_int32(int(k)), ctypes.c_int32(int(block)), _ptr(q),
+            ctypes.byref(ptrs), _ptr(seqlens), _ptr(k_per_seq), ctypes.c_void_p(role.data_ptr()),
+            _ptr(idx_in), _ptr(out), _ptr(idx_out), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel()), _ptr(device_error), _stream_handle(stream, dev))
+    _check(st, "lychee_hybrid_decode_attn_q8")
+    return out, idx_out
+
+
 def hardkuma_roles(alpha, beta, p=-0.1, q=1.1, layer0_retrieval=True, stream=None):
     """Head roles from HardKuma gate parameters: alpha, beta [L, Hq] float64 on
     one CUDA device.  Returns (roles [L, Hq] uint8 on that device, 1 = retrieval
@@ -346,7 +573,7 @@ class Profile:
     spans=True (lychee_profile_spans_begin) there is one ("attn_span", ms)
     record per stack call instead, and no event between its launches."""
     KINDS = {0: "attn", 1: "topk", 2: "combine", 3: "build_bits", 4: "export",
-             5: "topk+combine", 6: "attn_span"}
+             5: "topk+combine", 6: "attn_span", 7: "append"}
 
     def __init__(self, max_launches=4096, spans=False):
         self.max_launches = int(max_launches)

@@ -297,6 +297,139 @@ LYCHEE_API lychee_status lychee_hardkuma_roles(const double* alpha, const double
                                                double* expected_z, double* expected_l0,
                                                void* stream);
 
+/* ---- the 8-bit paged cache --------------------------------------------------------
+ * Keys and values in 8 bits, in pages: half the bytes of a bf16 cache for the
+ * part of the step that reads them, and memory taken page by page instead of
+ * B x N_max rows.  Three calls share it: an append that rotates (the position
+ * rotation of the keys and queries) and quantises, attention over every cached
+ * position, and the hybrid-head layer of lychee_hybrid_decode_attn.
+ *
+ * Layout of one layer's cache (k and v alike)
+ *   codes  [num_pages, Hkv, page, d] of 8 bits: LYCHEE_E4M3 (4 exponent and 3
+ *          mantissa bits, largest value 448, no infinities) or LYCHEE_INT8
+ *          (-127 .. 127)
+ *   scales [num_pages, Hkv] fp32: a block (the rows of one page and head) holds
+ *          code * scale
+ *   block_table [B, max_pages] int32: position j of sequence b is slot j % page
+ *          of page block_table[b][j / page].  Entries behind a sequence's last
+ *          page are not read.  Sequences may share pages that nothing is
+ *          appended to (a common prefix).
+ * Scales are powers of two 2^e, -60 <= e <= 60, as the append writes them.
+ * Attention takes any positive finite scale within that range.
+ *
+ * Supported: G = Hq / Hkv in {1, 2, 4, 8}, Hq <= 128, d in {64, 128}, page in
+ * {16, 32, 64, 128}, max_pages * page <= 2^24, num_pages * Hkv * page < 2^31.
+ *
+ * Conventions beyond those at the top of this file
+ *   - A sequence may be empty (seqlens[b] == 0): its outputs are zeros, its
+ *     retrieval heads hand on empty sets, and the append skips it.
+ *   - device_error: device uint32, or NULL.  Bits are OR-ed into it (those of
+ *     lychee_check_device_error: 1 = bad page number or bad incoming index, 2 =
+ *     bad sequence length; 16 = the append met a value that is not finite).  It
+ *     is never cleared here: the caller sets it to zero and reads it when it
+ *     likes.
+ *   - A page number outside [0, num_pages) is flagged and its rows are skipped.
+ */
+typedef enum { LYCHEE_E4M3 = 0, LYCHEE_INT8 = 1 } lychee_code;
+
+typedef struct {
+  int32_t B;         /* sequences                              */
+  int32_t Hq;        /* query heads                            */
+  int32_t Hkv;       /* key/value heads                        */
+  int32_t d;         /* head dimension                         */
+  int32_t page;      /* positions per page                     */
+  int32_t num_pages; /* pages of the cache                     */
+  int32_t max_pages; /* block table entries per sequence       */
+  int32_t dtype;     /* lychee_dtype of q, new rows and out    */
+  int32_t code;      /* lychee_code of the cache               */
+} lychee_q8_shape;
+
+typedef struct {
+  void* k;                     /* device [num_pages, Hkv, page, d] codes, 16-byte aligned */
+  void* v;
+  float* k_scale;              /* device [num_pages, Hkv] */
+  float* v_scale;
+  const int32_t* block_table;  /* device [B, max_pages]   */
+} lychee_q8_cache;
+
+/* New tokens, one after another: those of sequence b are tokens cu_new[b] ..
+ * cu_new[b + 1] - 1, or token b alone when cu_new is NULL.  Rows of one token
+ * are contiguous; from one token to the next it is *_stride elements (a
+ * multiple of 16 bytes), so k, v and q may be parts of one projection output. */
+typedef struct {
+  const void* k;          /* device [T, Hkv, d] dtype, 16-byte aligned          */
+  const void* v;          /* device [T, Hkv, d] dtype                           */
+  const void* q;          /* device [T, Hq, d] dtype, or NULL                   */
+  void* q_out;            /* device [T, Hq, d] dtype, contiguous; NULL iff q is */
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t q_stride;
+  const float* cos_sin;   /* device [n_pos, rot]: rot / 2 cosines, then rot / 2 sines
+                             of each position's angles; NULL: no rotation       */
+  const int32_t* cu_new;  /* device [B + 1], ascending, or NULL (then T == B)   */
+  int32_t T;              /* tokens                                             */
+  int32_t n_pos;          /* positions of cos_sin                               */
+  int32_t rot;            /* rotated dimensions: a multiple of 8, 8 .. d        */
+  int32_t interleaved;    /* 0: pairs (i, i + rot / 2); 1: pairs (2i, 2i + 1)   */
+} lychee_q8_tokens;
+
+/* New keys and values into the cache, rotated and quantised, and the queries
+ * rotated beside them.  With m_b new tokens, seqlens[b] = n_b counts them, and
+ * token i of them has position n_b - m_b + i.
+ *   rotation   y1 = x1 c - x2 s, y2 = x2 c + x1 s on keys and queries, in fp32,
+ *              each product and sum rounded once; dimensions past rot unchanged
+ *   scale      2^e, e = ceil(log2(amax / M)) within [-60, 60], amax the largest
+ *              magnitude among the block's new rows, M = 448 or 127; a block that
+ *              already holds rows of the sequence keeps the larger of its old and
+ *              the new scale, and when that grows its old codes are rounded to
+ *              the new one (c * old / new, to nearest even).  A block whose rows
+ *              begin with this call forgets what its page held.
+ *   code       y / scale to nearest even, saturated.  A NaN is stored as 0 and an
+ *              infinity as the largest value (neither sets the scale); both set
+ *              bit 16 of *device_error
+ *   q_out      rotated queries, rounded to dtype; rows of tokens that no sequence
+ *              owns (from cu_new[B] to T) are left as they are
+ * seqlens device [B].  A sequence whose numbers do not fit (m_b > n_b, n_b beyond
+ * max_pages * page, or beyond n_pos when there is a rotation) is skipped and
+ * flagged.  A page that takes new rows must belong to one sequence alone. */
+LYCHEE_API lychee_status lychee_append_rope_q8(const lychee_q8_shape* s, const lychee_q8_cache* cache,
+                                               const lychee_q8_tokens* tokens, const int32_t* seqlens,
+                                               uint32_t* device_error, void* stream);
+
+/* Bytes of device workspace for lychee_decode_attn_q8 (k = 0) or
+ * lychee_hybrid_decode_attn_q8 with index rows of capacity k.  0 if *s or k is
+ * invalid. */
+LYCHEE_API size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k);
+
+/* Attention of one query token a sequence over every cached position:
+ * out[b, h] = softmax(q . K_g^T / sqrt(d)) V_g over positions j < seqlens[b].
+ *   q, out    device [B, Hq, d] dtype, 16-byte aligned
+ *   workspace device, >= lychee_q8_workspace_size(s, 0) bytes, 256-byte aligned
+ * Scores are exact products of the codes with q (bf16), or with q held in two
+ * 11-bit parts (fp32), summed in fp32; softmax and sums are fp32. */
+LYCHEE_API lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q,
+                                               const lychee_q8_cache* cache, const int32_t* seqlens,
+                                               void* out, void* workspace, size_t workspace_bytes,
+                                               uint32_t* device_error, void* stream);
+
+/* lychee_hybrid_decode_attn over the 8-bit cache: retrieval heads attend to every
+ * position and hand on argsTopK of their logits (or whole blocks of `block`
+ * positions), sparse heads attend to their incoming set and hand it on.
+ *   k          capacity of an index row, 1 .. max_pages * page
+ *   block      as lychee_shape.block
+ *   k_per_seq, head_role, idx_in, idx_out as in lychee_hybrid_decode_attn; a sparse
+ *              head reads its entries before the first -1 (strictly ascending, below
+ *              n_b; one that is not is flagged, and what the head then returns is
+ *              unspecified).  An empty set gives zeros.
+ *   workspace  device, >= lychee_q8_workspace_size(s, k) bytes, 256-byte aligned */
+LYCHEE_API lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, int32_t block,
+                                               const void* q, const lychee_q8_cache* cache,
+                                               const int32_t* seqlens, const int32_t* k_per_seq,
+                                               const uint8_t* head_role, const int32_t* idx_in,
+                                               void* out, int32_t* idx_out, void* workspace,
+                                               size_t workspace_bytes, uint32_t* device_error,
+                                               void* stream);
+
 /* Synchronises `stream`, reads the device error word of `workspace` and clears
  * it.  Returns LYCHEE_OK, LYCHEE_ERR_BAD_INDEX, LYCHEE_ERR_TIMEOUT or
  * LYCHEE_ERR_CUDA.  If detail is not NULL it receives the raw flag bits
@@ -317,7 +450,7 @@ LYCHEE_API int32_t lychee_version(void);
  * (0 attention, 1 top-k, 2 combine, 3 set->bitmap, 4 bitmap->set, 5 the
  * retrieval heads' selection -- argsTopK, or the block selection when
  * s->block > 1 -- and the combine in one launch; in a stack, 1 is the
- * selection alone) and the
+ * selection alone; 7 the rotating append) and the
  * elapsed milliseconds; *n_out receives n.  Process-global state: one profiling
  * session at a time.  Events are created on the current device on first use
  * and kept for reuse. */
