@@ -34,18 +34,29 @@ struct Q8AppendParams {
 cudaError_t launch_q8_append(const Q8AppendParams& p, int dtype, int code, int D, cudaStream_t st);
 
 // Attention of one query token a sequence over the cache (q8_attn.cu).
+constexpr int kQ8Warps = 16;       // warps of an attention CTA (one CTA an SM)
+constexpr int kQ8MaxCtas = 160;    // attention CTAs at most (the workspace holds that many states)
+constexpr int kQ8MinSlabs = 2;     // slabs of 16 rows a warp takes at least, while there are any
+constexpr int kQ8Run = 256;        // positions of a run (hybrid: the unit whose rows are listed)
 struct Q8AttnParams {
   Q8Cache c;
   const void* q;             // [B, Hq, D]
   void* out;                 // [B, Hq, D]
   const int32_t* seqlens;    // [B]
-  const int32_t* idx_in;     // [B, Hq, k] or null: sets of the sparse heads
-  int32_t* idx_out;          // [B, Hq, k] or null
-  float* logits;             // [B, Hq, N_max] or null: raw q.k of the retrieval heads
-  uint32_t* err;
-  int B, Hq, Hkv, N_max, k;
+  uint32_t* err;             // or null
+  float* parts;              // [CTAs, 2, G * (D + 2)]: states a CTA left open: of a segment that
+                             // began before it, of one that began in it; m[G], l[G], acc[G][D]
+  int32_t* part_seg;         // [CTAs, 2]: their segments (sequence * Hkv + KV head), -1: none
+  float* scratch;            // [CTAs, kQ8Warps, G * (D + 2)]: a state a warp ended on its way
+  int B, Hq, Hkv, N_max;
   float scale_log2;          // log2(e) / sqrt(D)
   uint32_t role[4];          // bit h set: head h attends to every position
+  // hybrid layer only (run_slabs null: every head attends to every position)
+  uint8_t* run_slabs;        // [n_run_items * 16]: slabs of each run, [B * Hkv, runs_stride] of them
+  const uint32_t* bitmaps;   // [B, Hq, nwords]: the sparse heads' sets
+  float* logits;             // [B, Hq, N_max]: raw q.k of the retrieval heads
+  const int32_t* k_per_seq;  // [B] or null (checked here)
+  int nwords, runs_stride, n_run_items;
 };
 cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms,
                            cudaStream_t st);

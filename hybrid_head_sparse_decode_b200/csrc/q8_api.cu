@@ -30,6 +30,9 @@ lychee_status check_q8_shape(const lychee_q8_shape* s) {
   // rows are counted in 32 bits
   if ((long long)s->num_pages * s->Hkv * s->page > 0x7fffffffLL) return LYCHEE_ERR_UNSUPPORTED;
   if ((long long)s->B * s->Hq >= (1LL << 24)) return LYCHEE_ERR_UNSUPPORTED;
+  // runs of 256 positions, over all sequences and heads, are counted in 32 bits too
+  if ((long long)s->B * s->Hkv * (((long long)s->max_pages * s->page + kQ8Run - 1) / kQ8Run) > 0x7fffffffLL)
+    return LYCHEE_ERR_UNSUPPORTED;
   return LYCHEE_OK;
 }
 
@@ -56,14 +59,34 @@ Q8Cache cache_of(const lychee_q8_shape* s, const lychee_q8_cache* c) {
 
 int n_max_of(const lychee_q8_shape* s) { return s->max_pages * s->page; }
 
-// Workspace: for the hybrid step (k > 0), the retrieval heads' logits.
+// Workspace: the states that the attention CTAs leave open; for the hybrid step
+// (k > 0) also the retrieval heads' logits, the sparse heads' bitmaps and the
+// slab counts of the runs.
 struct Q8Layout {
-  size_t logits, total;
+  size_t part_seg, parts, scratch, logits, bitmaps, run_slabs, total;
+  int nwords, runs_stride, n_run_items;
 };
 Q8Layout q8_layout(const lychee_q8_shape* s, int k) {
   Q8Layout L{};
-  L.logits = 0;
-  L.total = 256 + (k > 0 ? align256((size_t)s->B * s->Hq * n_max_of(s) * 4) : 0);
+  const size_t state = (size_t)(s->Hq / s->Hkv) * (s->d + 2) * 4;
+  size_t at = align256(kQ8MaxCtas * 2 * sizeof(int32_t));
+  L.parts = at;
+  at += align256(kQ8MaxCtas * 2 * state);
+  L.scratch = at;
+  at += align256(kQ8MaxCtas * kQ8Warps * state);
+  if (k > 0) {
+    const size_t n_max = n_max_of(s);
+    L.nwords = (int)((n_max + 31) / 32);
+    L.runs_stride = (int)((n_max + kQ8Run - 1) / kQ8Run);
+    L.n_run_items = (int)(((long long)s->B * s->Hkv * L.runs_stride + 15) / 16);
+    L.logits = at;
+    at += align256((size_t)s->B * s->Hq * n_max * 4);
+    L.bitmaps = at;
+    at += align256((size_t)s->B * s->Hq * L.nwords * 4);
+    L.run_slabs = at;
+    at += align256((size_t)L.n_run_items * 16);
+  }
+  L.total = at;
   return L;
 }
 
@@ -78,8 +101,13 @@ lychee_status check_sets(const lychee_q8_shape* s, int k, int block) {
 }
 
 Q8AttnParams attn_params(const lychee_q8_shape* s, const void* q, const lychee_q8_cache* c,
-                         const int32_t* seqlens, void* out, uint32_t* err) {
+                         const int32_t* seqlens, void* out, uint32_t* err, const Q8Layout& L,
+                         void* workspace) {
   Q8AttnParams p{};
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.part_seg = reinterpret_cast<int32_t*>(ws + L.part_seg);
+  p.parts = reinterpret_cast<float*>(ws + L.parts);
+  p.scratch = reinterpret_cast<float*>(ws + L.scratch);
   p.c = cache_of(s, c);
   p.q = q;
   p.out = out;
@@ -150,11 +178,12 @@ lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q, con
   if (!q || !seqlens || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(seqlens, 4) ||
       !aligned(device_error, 4))
     return LYCHEE_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < q8_layout(s, 0).total || !aligned(workspace, 256))
+  const Q8Layout L = q8_layout(s, 0);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
     return LYCHEE_ERR_WORKSPACE;
   const int sms = num_sms_current();
   if (sms <= 0) return LYCHEE_ERR_CUDA;
-  Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error);
+  Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);
   for (int i = 0; i < 4; ++i) p.role[i] = 0xffffffffu;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
@@ -181,13 +210,32 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return LYCHEE_ERR_WORKSPACE;
   const int sms = num_sms_current();
   if (sms <= 0) return LYCHEE_ERR_CUDA;
-  Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error);
-  p.idx_in = idx_in;
-  p.idx_out = idx_out;
-  p.k = k;
-  p.logits = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.logits);
+  Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  uint32_t* bitmaps = reinterpret_cast<uint32_t*>(ws + L.bitmaps);
+  p.run_slabs = ws + L.run_slabs;
+  p.bitmaps = bitmaps;
+  p.logits = reinterpret_cast<float*>(ws + L.logits);
+  p.k_per_seq = k_per_seq;
+  p.nwords = L.nwords;
+  p.runs_stride = L.runs_stride;
+  p.n_run_items = L.n_run_items;
   fill_roles(p.role, head_role, s->Hq);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (ns > 0) {
+    // the incoming sets as bitmaps; the rows go on as they came
+    BuildBitsParams bp{};
+    bp.idx_in = idx_in;
+    bp.idx_out = idx_out;
+    bp.seqlens = seqlens;
+    bp.bitmaps = bitmaps;
+    bp.err = p.err;
+    bp.B = s->B; bp.Hq = s->Hq; bp.N_max = p.N_max; bp.nwords = L.nwords; bp.k = k;
+    bp.empty_ok = 1;
+    for (int h = 0; h < s->Hq; ++h)
+      if (head_role[h] == LYCHEE_ROLE_SPARSE) bp.heads[bp.nheads++] = (uint8_t)h;
+    if (timed(kKindBuildBits, cs, [&] { return launch_build_bits(bp, cs); }) != cudaSuccess) return LYCHEE_ERR_CUDA;
+  }
   if (timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); }) != cudaSuccess)
     return LYCHEE_ERR_CUDA;
   if (ns == s->Hq) return LYCHEE_OK;
@@ -198,7 +246,7 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   tp.k_per_seq = k_per_seq;
   tp.idx_out = idx_out;
   tp.err = p.err;
-  tp.B = s->B; tp.Hq = s->Hq; tp.N_max = p.N_max; tp.nwords = (p.N_max + 31) / 32; tp.k = k;
+  tp.B = s->B; tp.Hq = s->Hq; tp.N_max = p.N_max; tp.nwords = L.nwords; tp.k = k;
   tp.sms = sms;
   tp.empty_ok = 1;
   for (int h = 0; h < s->Hq; ++h)

@@ -1,133 +1,1005 @@
 // q8_attn.cu -- attention of one query token a sequence over the 8-bit paged
-// cache.
+// cache: every position (decode_attn_q8), or a hybrid-head layer whose sparse
+// heads read their sets only.
 //
-// Mathematics.  s_j = (q . c_j) sk / sqrt(d) with c_j the codes of key j and sk
-// the scale of its block; p = softmax(s) over every j < n_b (a head that attends
-// to everything) or over the head's set; out = sum_j p_j sv c'_j with the codes
-// and scales of the values.  A sequence of no rows and an empty set give zeros.
+// Mathematics.  With c_j, c'_j the codes of key and value j and sk, sv the scales
+// of their blocks: s_j = (q . c_j) sk / sqrt(d), p = softmax(s) over every j < n_b
+// (or over the head's set), out = sum_j p_j sv c'_j.  A sequence of no rows and an
+// empty set give zeros.  Codes become halves exactly (e4m3 and int8 both fit 11
+// bits), so both products run on the tensor cores without a second rounding of
+// the cache: q is scaled by a power of two into the halves' range (bf16 fits;
+// fp32 is held in two halves, 22 bits), q . c_j is summed in fp32 and takes the
+// scales afterwards.  The weight that multiplies the codes is w_j = p_j sv_j; it
+// is what must fit a half, so the running reference of the online softmax is the
+// maximum of s_j log2(e) + log2(sv_j), and the normaliser sums p_j beside it.
+// The reference is kept 6 below the maximum seen (weights up to 2^7) and moved
+// only when a weight would pass 2^15: weights down to 2^-31 of the largest keep
+// a place in the half's range.  With bf16 queries a weight is rounded to 11 bits
+// (the output has 8); with fp32 ones it is held in two halves.
 //
-// One CTA per (sequence, query head), one warp per row, an online softmax per
-// warp in fp32, the warps' states merged at the end.
+// Work split.  The unit is a slab of 16 rows of one KV head.  All slabs of the
+// call, ordered by sequence, head and position, are cut into one equal range per
+// CTA and that into one per warp, whatever the lengths (a sequence's and a head's
+// slabs are a segment; a hybrid layer counts only the rows that some head of the
+// group uses).  A warp works alone: it copies its slabs' rows into a ring of its
+// own in shared memory (cp.async, each lane exactly the bytes it will read, so
+// the ring needs no barrier but the warp's) and runs the G heads of the group
+// over each slab at once.  At the end the CTA merges its warps' states of a
+// segment, writes what is complete and leaves at most two states open: of a
+// segment that began in an earlier CTA and of one that goes on in a later CTA.
+// The second kernel merges those.  All sums have a fixed order.
+//
+// Layouts.  S = K q^T as mma.m16n8k16 with the slab's rows as M: a lane takes 16
+// consecutive bytes of rows r = lane / 4 and r + 8 (chunk lane % 4); which
+// dimension a k index means is free as long as q agrees, so its words convert to
+// A fragments in place.  O^T = V^T P with the dimensions as M: a lane takes chunk
+// lane / 4 of rows 2c, 2c + 1, 2c + 8, 2c + 9 (c = lane % 4); interleaving the
+// bytes of two rows gives the pairs along k that A wants.  P moves from the
+// accumulator layout to B by a transpose of 8x8 halves (movmatrix).
+#include <algorithm>
+
 #include "q8.cuh"
 
 namespace lychee {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kWarps = kQ8Warps;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
+constexpr float kRefSlack = 14.f;    // and moves when a weight passes it by more than this
+
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8z(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4z(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_u(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+               "{%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 template <typename T>
-__device__ __forceinline__ float load1(const T* p);
+__device__ __forceinline__ float4 load_q4(const T* p);
 template <>
-__device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float4 load_q4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
 template <>
-__device__ __forceinline__ float load1<float>(const float* p) { return *p; }
+__device__ __forceinline__ float4 load_q4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-template <typename T, int CODE, int D>
-__global__ void __launch_bounds__(kThreads) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  constexpr int E = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_acc[kWarps][D];
-  const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
-  const int G = p.Hq / p.Hkv, g = h / G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_raw = p.seqlens[b];
-  const int n = min(max(n_raw, 0), p.N_max);
-  if (threadIdx.x == 0 && h == 0 && n != n_raw) flag_error(p.err, kErrBadSeqlen);
-  const bool all = (p.role[h >> 5] >> (h & 31)) & 1u;
-  const int32_t* set = p.idx_in + (size_t)bh * p.k;
-  const T* q = static_cast<const T*>(p.q) + (size_t)bh * D + lane * E;
-  float qr[E], acc[E];
-  for (int e = 0; e < E; ++e) {
-    qr[e] = load1(q + e);
-    acc[e] = 0.f;
+template <typename T, int D, int G>
+struct Cfg {
+  static constexpr bool kTwo = sizeof(T) == 4;           // q and the weights in two halves
+  static constexpr bool kBeside = kTwo && G <= 4;        // ... in columns 0-3 and 4-7 of one product
+  static constexpr int NQ = kTwo && !kBeside ? 2 : 1;    // ... or in two products
+  static constexpr int KM = D / 16;                      // products along d (S), blocks of 16 dimensions (O)
+  static constexpr int KS = D / 32;                      // 16-byte pieces of K a lane takes of a slab
+  static constexpr int VB = D / 8;                       // bytes of V a lane takes of each of its four rows
+  static constexpr int OFF_V = 16 * D, OFF_S = 32 * D, OFF_META = OFF_S + 128, OFF_HEAD = OFF_META + 64;
+  static constexpr int STAGE = OFF_HEAD + 16;
+  static constexpr int LIST = kQ8Run * 2;                // a run's rows (hybrid): u16 each
+  static constexpr int WARP = kStages * STAGE + LIST;
+  static constexpr int STATE = G * (D + 2);              // floats of a state: m[G], l[G], acc[G][D]
+  static constexpr int SMEM = kWarps * WARP;
+  static_assert(STAGE % 16 == 0 && LIST % 16 == 0, "16-byte copies");
+  static_assert(kWarps * STATE * 4 <= SMEM, "the states are merged where the rings were");
+};
+
+// Where a range of slabs begins.
+struct Start {
+  int seg, run, slab;   // segment b * Hkv + g; hybrid: run of the segment, slab of the run
+};
+
+// A warp's place in its slabs: the next one to copy.
+struct Cursor {
+  int seg, b, g, n;
+  int at, count;        // dense: slab of the segment, slabs of it.  hybrid: slab of the run, slabs of it
+  int run, runs;        // hybrid
+  int rows;             // hybrid: rows of the run
+  bool packed;          // hybrid: the run's rows are consecutive
+  int win;              // dense: the slab that lane 0's table entry belongs to
+  int page;             // this lane's table entry of the window / run
+};
+
+template <typename T, int CODE, int D, int G, bool HYB>
+struct Warp {
+  using C = Cfg<T, D, G>;
+  const Q8AttnParams& p;
+  uint32_t ring, list;
+  int lane, r, c;
+  Cursor cur;
+
+  __device__ __forceinline__ Warp(const Q8AttnParams& pp, uint32_t base)
+      : p(pp), ring(base), list(base + kStages * C::STAGE) {
+    lane = threadIdx.x & 31;
+    r = lane >> 2;
+    c = lane & 3;
   }
-  float m = -INFINITY, l = 0.f;
-  const int rows = all ? n : p.k;
-  for (int i = warp; i < rows; i += kWarps) {
-    int pos = i;
-    if (!all) {
-      pos = set[i];
-      if (pos < 0) continue;   // past the set's end
-      if (pos >= n || (i > 0 && (pos <= set[i - 1] || set[i - 1] < 0))) {
-        flag_error(p.err, kErrBadIndex);
-        continue;
+  __device__ __forceinline__ int length(int b) const { return min(max(__ldg(&p.seqlens[b]), 0), p.N_max); }
+
+  // ---- the cursor
+  __device__ __forceinline__ void enter(int seg) {
+    cur.seg = seg;
+    cur.b = seg / p.Hkv;
+    cur.g = seg - cur.b * p.Hkv;
+    cur.n = length(cur.b);
+    cur.at = 0;
+    cur.win = -64;
+    if (HYB) {
+      cur.run = 0;
+      cur.runs = (cur.n + kQ8Run - 1) / kQ8Run;
+    } else {
+      cur.count = (cur.n + 15) >> 4;
+    }
+  }
+  // The first run at or after `from` that holds a row (`upto` if none does).
+  __device__ __forceinline__ int next_run(int seg, int from, int upto) const {
+    const uint8_t* s = p.run_slabs + (size_t)seg * p.runs_stride;
+    for (int i0 = from; i0 < upto; i0 += 128) {
+      uint32_t k[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 32 * j + lane;
+        k[j] = i < upto ? __ldcg(s + i) : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t m = __ballot_sync(kFull, k[j] != 0);
+        if (m) return i0 + 32 * j + __ffs(m) - 1;
       }
     }
-    const int page = p.c.table[(size_t)b * p.c.max_pages + (pos >> p.c.page_log2)];
-    if (page < 0 || page >= p.c.num_pages) {
-      flag_error(p.err, kErrBadIndex);
-      continue;
+    return upto;
+  }
+  // To the first segment after cur.seg that has positions; false if there is none.
+  __device__ __forceinline__ bool enter_next() {
+    int seg = cur.seg + 1;
+    while (seg < p.B * p.Hkv) {
+      enter(seg);
+      if (cur.n > 0) return true;
+      seg = (cur.b + 1) * p.Hkv;
     }
-    const size_t unit = (size_t)page * p.Hkv + g;
-    const size_t row = ((unit << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1))) * D;
-    float kx[4], vx[4];
-    if constexpr (E == 4) {
-      const float4 a = codes_to_float<CODE>(*reinterpret_cast<const uint32_t*>(p.c.k + row + lane * E));
-      const float4 c = codes_to_float<CODE>(*reinterpret_cast<const uint32_t*>(p.c.v + row + lane * E));
-      kx[0] = a.x; kx[1] = a.y; kx[2] = a.z; kx[3] = a.w;
-      vx[0] = c.x; vx[1] = c.y; vx[2] = c.z; vx[3] = c.w;
+    return false;
+  }
+  // The rows of run cur.run into the list: entry = position in the run | heads << 8.
+  __device__ __forceinline__ void build_run() {
+    const int base = cur.run * kQ8Run;
+    const int word = lane >> 2, shift = (lane & 3) * 8;   // eight positions a lane
+    const int pos0 = base + lane * 8;
+    const int left = min(max(cur.n - pos0, 0), 8);
+    const uint32_t in = (1u << left) - 1u;
+    const int lp = base >> p.c.page_log2;
+    const int pages = max(1, kQ8Run >> p.c.page_log2);
+    cur.page = lane < pages && lp + lane < p.c.max_pages
+                   ? __ldg(&p.c.table[(size_t)cur.b * p.c.max_pages + lp + lane]) : -1;
+    uint32_t bits[G], u = 0;
+#pragma unroll
+    for (int t = 0; t < G; ++t) {
+      const int h = cur.g * G + t;
+      if ((p.role[h >> 5] >> (h & 31)) & 1u) bits[t] = in;
+      else {
+        const int w = (base >> 5) + word;
+        const uint32_t x = w < p.nwords
+                               ? __ldcg(&p.bitmaps[((size_t)cur.b * p.Hq + h) * p.nwords + w]) : 0u;
+        bits[t] = (x >> shift) & in;
+      }
+      u |= bits[t];
+    }
+    const int mine = __popc(u);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    cur.rows = __shfl_sync(kFull, incl, 31);
+    cur.count = (cur.rows + 15) >> 4;
+    cur.packed = cur.rows == min(cur.n - base, kQ8Run);
+    int slot = incl - mine;
+    __syncwarp();   // the previous run's entries were read
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((u >> i) & 1u) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int t = 0; t < G; ++t) m |= ((bits[t] >> i) & 1u) << t;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(list + 2 * slot), "h"((uint16_t)((lane * 8 + i) | (m << 8))) : "memory");
+        ++slot;
+      }
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void begin(const Start& s) {
+    enter(s.seg);
+    if (HYB) {
+      cur.run = s.run;
+      build_run();
+    }
+    cur.at = s.slab;
+  }
+  // To the next slab.  false: there is none (never, unless lengths or sets change
+  // under the call).
+  __device__ __forceinline__ bool advance() {
+    if (++cur.at < cur.count) return true;
+    if (HYB) {
+      int run = next_run(cur.seg, cur.run + 1, cur.runs);
+      while (run >= cur.runs) {
+        if (!enter_next()) return false;
+        run = next_run(cur.seg, 0, cur.runs);
+      }
+      cur.run = run;
+      cur.at = 0;
+      build_run();
+      return true;
+    }
+    return enter_next();
+  }
+
+  // ---- copies of the slab at the cursor into stage `st`
+  __device__ __forceinline__ void copy_rows(uint32_t st, const uint8_t* kp, const uint8_t* vp) {
+    // kp: row r's chunk c, vp: row 2c's chunk r of sixteen consecutive rows
+    const uint32_t kd = st + lane * 16;
+#pragma unroll
+    for (int j = 0; j < C::KS; ++j) {
+      constexpr int half = C::KS / 2;
+      const int row = (j / half) * 8, col = (j % half) * 64;
+      cp_async16z(kd + j * 512, kp + row * D + col, 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = (j >> 1) * 8 + (j & 1);
+      if (C::VB == 16) cp_async16z(st + C::OFF_V + j * 512 + lane * 16, vp + row * D, 16);
+      else cp_async8z(st + C::OFF_V + j * 256 + lane * 8, vp + row * D, 8);
+    }
+  }
+  __device__ __forceinline__ void copy_gathered(uint32_t st, uint32_t myrow, uint32_t mysize) {
+    // lane i (and i + 16) knows row i
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t row = __shfl_sync(kFull, myrow, r + 8 * i), sz = __shfl_sync(kFull, mysize, r + 8 * i);
+      const uint8_t* src = p.c.k + (size_t)row * D + 16 * c;
+#pragma unroll
+      for (int j = 0; j < C::KS / 2; ++j) cp_async16z(st + (i * (C::KS / 2) + j) * 512 + lane * 16, src + 64 * j, sz);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 2 * c + (j >> 1) * 8 + (j & 1);
+      const uint32_t row = __shfl_sync(kFull, myrow, i), sz = __shfl_sync(kFull, mysize, i);
+      const uint8_t* src = p.c.v + (size_t)row * D + C::VB * r;
+      if (C::VB == 16) cp_async16z(st + C::OFF_V + j * 512 + lane * 16, src, sz);
+      else cp_async8z(st + C::OFF_V + j * 256 + lane * 8, src, sz ? 8u : 0u);
+    }
+  }
+  __device__ __forceinline__ void copy(uint32_t st) {
+    const int log2p = p.c.page_log2, pmask = (1 << log2p) - 1;
+    const int i = lane & 15;
+    const float* scales = lane < 16 ? p.c.k_scale : p.c.v_scale;
+    uint32_t meta;
+    if (!HYB || cur.packed) {
+      // sixteen consecutive positions, all in one page (pages are whole slabs)
+      int pos0, page;
+      if (HYB) {
+        pos0 = cur.run * kQ8Run + 16 * cur.at;
+        page = __shfl_sync(kFull, cur.page, (16 * cur.at) >> log2p);
+      } else {
+        pos0 = 16 * cur.at;
+        if ((unsigned)(cur.at - cur.win) >= 32u) {
+          cur.win = cur.at;
+          cur.page = cur.at + lane < cur.count
+                         ? __ldg(&p.c.table[(size_t)cur.b * p.c.max_pages + ((16 * (cur.at + lane)) >> log2p)]) : -1;
+        }
+        page = __shfl_sync(kFull, cur.page, cur.at - cur.win);
+      }
+      const int rows = min(16, cur.n - pos0);
+      const bool ok = page >= 0 && page < p.c.num_pages;
+      if (!ok && lane == 0) flag_error(p.err, kErrBadIndex);
+      const int unit = (ok ? page : 0) * p.Hkv + cur.g;
+      const uint32_t row0 = ((uint32_t)unit << log2p) + (pos0 & pmask);
+      if (ok && rows == 16) {
+        copy_rows(st, p.c.k + (size_t)row0 * D + r * D + 16 * c, p.c.v + (size_t)row0 * D + 2 * c * D + C::VB * r);
+      } else {
+        const bool in = ok && i < rows;
+        copy_gathered(st, row0 + (in ? i : 0), in ? 16u : 0u);
+      }
+      cp_async4z(st + C::OFF_S + lane * 4, scales + unit, ok ? 4u : 0u);
+      uint32_t heads = (1u << G) - 1u;
+      if (HYB && i < rows) {
+        uint16_t e;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * (16 * cur.at + i)));
+        heads = e >> 8;
+      }
+      meta = (uint32_t)(pos0 + i) | (ok && i < rows ? heads << 24 : 0u);
     } else {
-      const float4 a = codes_to_float<CODE>(*reinterpret_cast<const uint16_t*>(p.c.k + row + lane * E));
-      const float4 c = codes_to_float<CODE>(*reinterpret_cast<const uint16_t*>(p.c.v + row + lane * E));
-      kx[0] = a.x; kx[1] = a.y;
-      vx[0] = c.x; vx[1] = c.y;
+      const int e_at = 16 * cur.at + i;
+      uint16_t e = 0;
+      if (e_at < cur.rows) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * e_at));
+      const int off = e & 255;
+      const int page = __shfl_sync(kFull, cur.page, off >> log2p);
+      const bool in = e_at < cur.rows, ok = page >= 0 && page < p.c.num_pages;
+      if (in && !ok) flag_error(p.err, kErrBadIndex);
+      const int unit = (ok ? page : 0) * p.Hkv + cur.g;
+      const int pos = cur.run * kQ8Run + off;
+      copy_gathered(st, ((uint32_t)unit << log2p) + (pos & pmask), in && ok ? 16u : 0u);
+      cp_async4z(st + C::OFF_S + lane * 4, scales + unit, in && ok ? 4u : 0u);
+      meta = (uint32_t)pos | (in && ok ? (uint32_t)(e >> 8) << 24 : 0u);
     }
-    float dot = 0.f;
-    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], kx[e], dot);
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    dot *= p.c.k_scale[unit];
-    if (all && p.logits && lane == 0) p.logits[(size_t)bh * p.N_max + pos] = dot;
-    const float t = dot * p.scale_log2;
-    const float mn = fmaxf(m, t);
-    const float a = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(t - mn);
-    const float w = pr * p.c.v_scale[unit];
-    l = l * a + pr;
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, vx[e], acc[e] * a);
-    m = mn;
+    if (lane < 16) sts_u(st + C::OFF_META + lane * 4, meta);
+    if (lane == 16) sts_u(st + C::OFF_HEAD, (uint32_t)cur.seg);
   }
-  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+
+  // ---- the heads' states
+  uint32_t qf[C::NQ][C::KM][2];   // q as B fragments
+  float fq[2];                    // powers of two that undo q's scaling, of this lane's two columns
+  float ref[2], l[2];             // reference (log2) and sum of weights, of this lane's two columns
+  float acc[C::KM][4];
+
+  __device__ __forceinline__ int column_head(int j) const { return (C::kBeside ? 2 * (c & 1) : 2 * c) + j; }
+
+  __device__ __forceinline__ void load_q(int seg) {
+    const int b = seg / p.Hkv, g = seg - b * p.Hkv;
+    const int t = C::kBeside ? r & 3 : r;
+    float4 x[C::KM];
+    float mx = 0.f;
+#pragma unroll
+    for (int m = 0; m < C::KM; ++m) {
+      x[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < G)
+        x[m] = load_q4<T>(static_cast<const T*>(p.q) + ((size_t)b * p.Hq + g * G + t) * D + (m >> 2) * 64 +
+                          16 * c + 4 * (m & 3));
+      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x[m].x), fabsf(x[m].y)), fmaxf(fabsf(x[m].z), fabsf(x[m].w))));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+    // the largest magnitude to [2^13, 2^14) (below 2^-100 the same factor as at 2^-100)
+    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
+    const float up = exp2_int(13 - e), down = exp2_int(e - 13);
+#pragma unroll
+    for (int m = 0; m < C::KM; ++m) {
+      const float a = x[m].x * up, bb = x[m].y * up, cc = x[m].z * up, d = x[m].w * up;
+      uint32_t w0 = pack_half(a, bb), w1 = pack_half(cc, d);
+      if (C::kTwo) {
+        const float2 h0 = unpack_half(w0), h1 = unpack_half(w1);
+        const uint32_t l0 = pack_half(a - h0.x, bb - h0.y), l1 = pack_half(cc - h1.x, d - h1.y);
+        if (C::NQ == 2) {
+          qf[C::NQ - 1][m][0] = l0;
+          qf[C::NQ - 1][m][1] = l1;
+        } else if (r >= 4) {
+          w0 = l0;
+          w1 = l1;
+        }
+      }
+      qf[0][m][0] = w0;
+      qf[0][m][1] = w1;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fq[j] = __shfl_sync(kFull, down, (column_head(j) & 7) * 4);
   }
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int m = 0; m < C::KM; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+    ref[0] = ref[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // ---- one slab
+  __device__ __forceinline__ void consume(uint32_t st, int seg) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      float s2[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t ks = st + lane * 16;
+#pragma unroll
+      for (int h = 0; h < C::KS / 2; ++h) {
+        const uint4 lo = lds128(ks + h * 512), hi = lds128(ks + (C::KS / 2 + h) * 512);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int m = h * 4 + j;
+          uint32_t a0, a1, a2, a3;
+          codes_to_half<CODE>(wl[j], a0, a2);
+          codes_to_half<CODE>(wh[j], a1, a3);
+          mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[0][m][0], qf[0][m][1]);
+          if (C::NQ == 2) mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[C::NQ - 1][m][0], qf[C::NQ - 1][m][1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += s2[i];
+    }
+    if (C::kBeside) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(kFull, s[i], 2);
+    }
+    // s[0], s[1]: row r, columns 2c and 2c + 1; s[2], s[3]: row r + 8
+    float w[4], t[4];
+    float sv[2];
+    bool on[4];
+    bool over = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float sk = lds_f(st + C::OFF_S + (r + 8 * i) * 4);
+      sv[i] = lds_f(st + C::OFF_S + (16 + r + 8 * i) * 4);
+      const uint32_t meta = lds_u(st + C::OFF_META + (r + 8 * i) * 4);
+      const float ev = (float)((int)((__float_as_uint(sv[i]) >> 23) & 255u) - 127);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int h = column_head(j);
+        const float raw = s[2 * i + j] * sk * fq[j];
+        on[2 * i + j] = h < G && ((meta >> (24 + (h & 7))) & 1u);
+        if (HYB && h < G && p.logits && (!C::kBeside || c < 2)) {
+          const int b = seg / p.Hkv, hq = (seg - b * p.Hkv) * G + h;
+          if (on[2 * i + j] && ((p.role[hq >> 5] >> (hq & 31)) & 1u))
+            p.logits[((size_t)b * p.Hq + hq) * p.N_max + (meta & 0xffffffu)] = raw;
+        }
+        t[2 * i + j] = raw * p.scale_log2;
+        over = over || (on[2 * i + j] && t[2 * i + j] + ev > ref[j] + kRefSlack);
+      }
+    }
+    if (__any_sync(kFull, over)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float ev = (float)((int)((__float_as_uint(sv[i]) >> 23) & 255u) - 127);
+          if (on[2 * i + j]) mx = fmaxf(mx, t[2 * i + j] + ev);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+        if (mx > ref[j] + kRefSlack) {
+          const float to = mx - kRefBelow;
+          const float f = fast_exp2(ref[j] - to);   // 0 while the reference is -inf
+          l[j] *= f;
+#pragma unroll
+          for (int m = 0; m < C::KM; ++m) {
+            acc[m][j] *= f;
+            acc[m][2 + j] *= f;
+          }
+          ref[j] = to;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float e = on[2 * i + j] ? fast_exp2(t[2 * i + j] - ref[j]) : 0.f;
+        l[j] += e;
+        w[2 * i + j] = on[2 * i + j] ? e * sv[i] : 0.f;
+      }
+    uint32_t pb[C::NQ][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
+      if (C::kTwo) {
+        const float2 hf = unpack_half(hi);
+        const uint32_t lo = pack_half(w[2 * i] - hf.x, w[2 * i + 1] - hf.y);
+        if (C::NQ == 2) pb[C::NQ - 1][i] = movmatrix_trans(lo);
+        else if (c >= 2) hi = lo;
+      }
+      pb[0][i] = movmatrix_trans(hi);
+    }
+    // the values: words of rows 2c, 2c + 1, 2c + 8, 2c + 9
+    uint32_t v[4][C::VB / 4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (C::VB == 16) {
+        const uint4 x = lds128(st + C::OFF_V + j * 512 + lane * 16);
+        v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+      } else {
+        const uint2 x = lds64(st + C::OFF_V + j * 256 + lane * 8);
+        v[j][0] = x.x; v[j][1] = x.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < C::VB / 4; ++k) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half ? 0x7362u : 0x5140u;
+        uint32_t a0, a1, a2, a3;
+        codes_to_half<CODE>(__byte_perm(v[0][k], v[1][k], sel), a0, a1);
+        codes_to_half<CODE>(__byte_perm(v[2][k], v[3][k], sel), a2, a3);
+        mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[0][0], pb[0][1]);
+        if (C::NQ == 2) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[C::NQ - 1][0], pb[C::NQ - 1][1]);
+      }
+    }
+  }
+
+  // ---- the state: this lane's columns' sums complete in every lane
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(kFull, l[j], o);
+    if (C::kBeside) {
+#pragma unroll
+      for (int m = 0; m < C::KM; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] += __shfl_xor_sync(kFull, acc[m][i], 2);
+    }
+  }
+  // Dimension of acc[m][2 * i + j]: chunk r, byte 2 m + i of it.
+  __device__ __forceinline__ void write_out(int seg) {
+    finish();
+    const int b = seg / p.Hkv, g = seg - b * p.Hkv;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h = column_head(j);
+      if (h >= G || (C::kBeside && c >= 2)) continue;
+      const float inv = l[j] > 0.f ? 1.f / l[j] : 0.f;
+      T* o = static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + r * C::VB;
+#pragma unroll
+      for (int m = 0; m < C::KM; ++m) {
+        store1(o + 2 * m, acc[m][j] * inv);
+        store1(o + 2 * m + 1, acc[m][2 + j] * inv);
+      }
+    }
+  }
+  __device__ __forceinline__ void write_state(float* s) {
+    finish();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h = column_head(j);
+      if (h >= G || (C::kBeside && c >= 2)) continue;
+      if (r == 0) {
+        s[h] = ref[j];
+        s[G + h] = l[j];
+      }
+      float* o = s + 2 * G + h * D + r * C::VB;
+#pragma unroll
+      for (int m = 0; m < C::KM; ++m) {
+        o[2 * m] = acc[m][j];
+        o[2 * m + 1] = acc[m][2 + j];
+      }
+    }
+  }
+};
+
+// What a warp leaves for the CTA's merge.
+struct WarpEnd {
+  int ended;     // segment that began before the warp and ended in it (its state in global memory), or -1
+  int open;      // segment still open at the warp's end (its state in shared memory), or -1
+  int began;     // the open segment began in this warp
+};
+
+// One merged column over a chain of states.
+struct Chain {
+  float m, l, a;
+  __device__ __forceinline__ void clear() { m = -INFINITY; l = 0.f; a = 0.f; }
+  __device__ __forceinline__ void add(float m2, float l2, float a2) {
+    if (m2 == -INFINITY) return;
+    const float M = fmaxf(m, m2);
+    const float f = m == -INFINITY ? 0.f : fast_exp2(m - M), f2 = fast_exp2(m2 - M);
+    l = l * f + l2 * f2;
+    a = a * f + a2 * f2;
+    m = M;
+  }
+};
+
+__device__ __forceinline__ int warp_sum_int(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// Slabs of item i: of sequence i over all its KV heads (dense), of run i (hybrid;
+// sixteen runs to an item).
+template <bool HYB>
+__device__ __forceinline__ long long item_slabs(const Q8AttnParams& p, int i, int n_items) {
+  if (i >= n_items) return 0;
+  if (HYB) {
+    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(p.run_slabs) + i);
+    return (long long)__dp4a(x.x, 0x01010101u, __dp4a(x.y, 0x01010101u, __dp4a(x.z, 0x01010101u, __dp4a(x.w, 0x01010101u, 0u))));
+  }
+  const int n = min(max(__ldg(&p.seqlens[i]), 0), p.N_max);
+  return (long long)((n + 15) >> 4) * p.Hkv;
+}
+
+template <typename T, int CODE, int D, int G, bool HYB>
+__global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
+  using C = Cfg<T, D, G>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long s_wsum[kWarps];
+  __shared__ Start s_start[kWarps];
+  __shared__ WarpEnd s_end[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- how many slabs there are, and where each warp's begin
+  const int n_items = HYB ? p.n_run_items : p.B;
+  long long total = 0;
+  {
+    long long mine = 0;
+    for (int i = tid; i < n_items; i += kThreads) mine += item_slabs<HYB>(p, i, n_items);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
+    if (lane == 0) s_wsum[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_wsum[w];
+    __syncthreads();
+  }
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.B; b += kThreads) {
+      const int n = __ldg(&p.seqlens[b]);
+      if (n < 0 || n > p.N_max) flag_error(p.err, kErrBadSeqlen);
+      if (HYB && p.k_per_seq && n > 0 && __ldg(&p.k_per_seq[b]) < 1) flag_error(p.err, kErrBadBudget);
+    }
+  if (!HYB) {
+    // sequences of no rows give zeros
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+      if (__ldg(&p.seqlens[b]) <= 0)
+        for (int i = tid; i < p.Hq * D; i += kThreads) store1(static_cast<T*>(p.out) + (size_t)b * p.Hq * D + i, 0.f);
+  }
+  // ranges: per CTA, then per warp, at least kQ8MinSlabs a warp
+  const long long per_cta = max((total + gridDim.x - 1) / gridDim.x, (long long)kQ8MinSlabs * kWarps);
+  const long long c0 = min(total, per_cta * blockIdx.x), c1 = min(total, c0 + per_cta);
+  const long long per_warp = (c1 - c0 + kWarps - 1) / kWarps;
+  const long long w0 = min(c1, c0 + per_warp * warp);
+  int mine = (int)(min(c1, w0 + per_warp) - w0);
+  if (c1 > c0) {
+    long long before = 0;
+    for (int i0 = 0; i0 < n_items && before < c1; i0 += kThreads) {
+      const long long v = item_slabs<HYB>(p, i0 + tid, n_items);
+      long long incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_wsum[warp] = incl;
+      __syncthreads();
+      long long round = 0, off = before;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) off += s_wsum[w];
+        round += s_wsum[w];
+      }
+      const long long lo = off + incl - v, hi = off + incl;   // this item's slabs
+      if (v > 0 && hi > c0 && lo < c1) {
+        int w = lo > c0 ? (int)((lo - c0 + per_warp - 1) / per_warp) : 0;
+        for (; w < kWarps && c0 + w * per_warp < min(hi, c1); ++w) {
+          long long rel = c0 + w * per_warp - lo;
+          Start s;
+          if (HYB) {
+            int run = (i0 + tid) * 16;
+            int k = __ldcg(&p.run_slabs[run]);
+            while (rel >= k && run < (i0 + tid) * 16 + 15) {
+              rel -= k;
+              k = __ldcg(&p.run_slabs[++run]);
+            }
+            s.seg = run / p.runs_stride;
+            s.run = run - s.seg * p.runs_stride;
+            s.slab = (int)rel;
+          } else {
+            const int len = (int)(v / p.Hkv);
+            s.seg = (i0 + tid) * p.Hkv + (int)(rel / len);
+            s.run = 0;
+            s.slab = (int)(rel % len);
+          }
+          s_start[w] = s;
+        }
+      }
+      before += round;
+      __syncthreads();
+    }
+  }
+
+  // ---- the warp's slabs
+  const uint32_t base = smem_u32(smem) + warp * C::WARP;
+  WarpEnd end{-1, -1, 0};
+  float* scratch = p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE;
+  Warp<T, CODE, D, G, HYB> wk(p, base);
+  if (mine > 0) {
+    const Start s0 = s_start[warp];
+    wk.begin(s0);
+    // does the first segment begin here?
+    bool began = s0.slab == 0;
+    if (HYB && began) began = wk.next_run(s0.seg, 0, s0.run) >= s0.run;
+    int copied = 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (copied > 0 && copied < mine && !wk.advance()) mine = copied;
+      if (copied < mine) {
+        wk.copy(base + i * C::STAGE);
+        ++copied;
+      }
+      cp_async_commit();
+    }
+    int seg = -1;
+    uint32_t st = base, st_in = base + (kStages - 1) * C::STAGE;
+    const uint32_t ring_end = base + kStages * C::STAGE;
+    for (int i = 0; i < mine; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      const int now = (int)lds_u(st + C::OFF_HEAD);
+      if (now != seg) {
+        if (seg >= 0) {
+          if (began) wk.write_out(seg);
+          else {
+            wk.write_state(scratch);
+            end.ended = seg;
+          }
+          began = true;
+        }
+        seg = now;
+        wk.load_q(seg);
+        wk.reset();
+      }
+      if (copied < mine && !wk.advance()) mine = copied;
+      if (copied < mine) {
+        wk.copy(st_in);
+        ++copied;
+      }
+      cp_async_commit();
+      wk.consume(st, seg);
+      st += C::STAGE;
+      if (st == ring_end) st = base;
+      st_in += C::STAGE;
+      if (st_in == ring_end) st_in = base;
+      __syncwarp();   // the stage is free to be written
+    }
+    // is the last segment complete?  (the cursor stands on its last copied slab)
+    bool last = wk.cur.at + 1 >= wk.cur.count;
+    if (HYB && last) last = wk.next_run(seg, wk.cur.run + 1, wk.cur.runs) >= wk.cur.runs;
+    if (last && began) wk.write_out(seg);
+    else if (last) {
+      wk.write_state(scratch);
+      end.ended = seg;
+    } else {
+      end.open = seg;
+      end.began = began;
+    }
+  }
+  if (lane == 0) s_end[warp] = end;
+  __syncthreads();   // every ring is drained
+  float* states = reinterpret_cast<float*>(smem);
+  if (end.open >= 0) wk.write_state(states + warp * C::STATE);
   __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY, L = 0.f, A = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
+
+  // ---- merge: chains of states of one segment across the CTA's warps
+  int part_seg[2] = {-1, -1};
+  for (int col = tid; col < G * D; col += kThreads) {
+    const int h = col / D, e = col - h * D;
+    Chain ch;
+    ch.clear();
+    int cseg = -1;
+    bool cbegan = false;
+    auto leave = [&](int slot) {   // an incomplete chain goes to the CTA's slot
+      float* s = p.parts + ((size_t)blockIdx.x * 2 + slot) * C::STATE;
+      s[2 * G + col] = ch.a;
+      if (e == 0) {
+        s[h] = ch.m;
+        s[G + h] = ch.l;
+      }
+    };
+    part_seg[0] = part_seg[1] = -1;
     for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-      L = fmaf(f, s_l[w], L);
-      A = fmaf(f, s_acc[w][threadIdx.x], A);
+      const WarpEnd we = s_end[w];
+      if (we.ended >= 0) {
+        const float* s = p.scratch + ((size_t)blockIdx.x * kWarps + w) * C::STATE;
+        ch.add(s[h], s[G + h], s[2 * G + col]);
+        if (cbegan) {
+          const int b = we.ended / p.Hkv, g = we.ended - b * p.Hkv;
+          store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + e, ch.l > 0.f ? ch.a / ch.l : 0.f);
+        } else {
+          leave(0);
+          part_seg[0] = we.ended;
+        }
+        ch.clear();
+        cseg = -1;
+        cbegan = false;
+      }
+      if (we.open >= 0) {
+        const float* s = states + w * C::STATE;
+        if (we.began) cbegan = true;
+        cseg = we.open;
+        ch.add(s[h], s[G + h], s[2 * G + col]);
+      }
     }
-    store1(static_cast<T*>(p.out) + (size_t)bh * D + threadIdx.x, L > 0.f ? A / L : 0.f);
+    if (cseg >= 0) {
+      leave(cbegan ? 1 : 0);
+      part_seg[cbegan ? 1 : 0] = cseg;
+    }
   }
-  // a set goes on as it came
-  if (p.idx_out) {
-    for (int i = threadIdx.x; i < p.k; i += kThreads)
-      if (!all) p.idx_out[(size_t)bh * p.k + i] = set[i];
+  if (tid == 0) {
+    p.part_seg[2 * blockIdx.x] = part_seg[0];
+    p.part_seg[2 * blockIdx.x + 1] = part_seg[1];
   }
 }
 
-template <typename T, int CODE>
-cudaError_t launch_c(const Q8AttnParams& p, int D, cudaStream_t st) {
-  const dim3 grid((unsigned)(p.B * p.Hq));
-  const cudaError_t e = D == 128 ? launch_pdl(q8_attn_kernel<T, CODE, 128>, grid, dim3(kThreads), 0, st, p)
-                                 : launch_pdl(q8_attn_kernel<T, CODE, 64>, grid, dim3(kThreads), 0, st, p);
+// ---- the states that attention CTAs left open ------------------------------------------
+// Grid (attention CTAs, G): block (x, h) merges head h of the segment that CTA x
+// left in its slot 1, with the states that later CTAs left of it in slot 0.  A
+// thread group of D / 4 lanes takes every kGroups-th state, then the groups'
+// states are merged in order.
+constexpr int kMergeThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
+  constexpr int LPS = D / 4;                 // lanes a state
+  constexpr int kGroups = kMergeThreads / LPS;
+  __shared__ float s_acc[kGroups][D], s_m[kGroups], s_l[kGroups];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int first = blockIdx.x, h = blockIdx.y, ctas = gridDim.x, G = gridDim.y;
+  const int seg = p.part_seg[2 * first + 1];
+  if (seg < 0) return;
+  int more = 0;
+  for (int i0 = first + 1; i0 < ctas; i0 += kMergeThreads) {
+    const int i = i0 + threadIdx.x;
+    const int got = __syncthreads_count(i < ctas && p.part_seg[2 * i] == seg);
+    more += got;
+    if (got < min(kMergeThreads, ctas - i0)) break;
+  }
+  const int group = threadIdx.x / LPS, col = (threadIdx.x % LPS) * 4;
+  const int stride = G * (D + 2);
+  Chain ch[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) ch[j].clear();
+  for (int i = group; i <= more; i += kGroups) {
+    const float* s = p.parts + ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * stride;
+    const float m = s[h], l = s[G + h];
+    const float2 a = *reinterpret_cast<const float2*>(s + 2 * G + h * D + col);
+    const float2 b = *reinterpret_cast<const float2*>(s + 2 * G + h * D + col + 2);
+    ch[0].add(m, l, a.x);
+    ch[1].add(m, l, a.y);
+    ch[2].add(m, l, b.x);
+    ch[3].add(m, l, b.y);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s_acc[group][col + j] = ch[j].a;
+  if (col == 0) {
+    s_m[group] = ch[0].m;
+    s_l[group] = ch[0].l;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    Chain t;
+    t.clear();
+    for (int i = 0; i < kGroups; ++i) t.add(s_m[i], s_l[i], s_acc[i][threadIdx.x]);
+    const int b = seg / p.Hkv, g = seg - b * p.Hkv;
+    store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + threadIdx.x, t.l > 0.f ? t.a / t.l : 0.f);
+  }
+}
+
+// ---- hybrid: slabs of every run -------------------------------------------------------------
+// A run is kQ8Run positions of one segment; its rows are those that some head of
+// the group uses: all below n_b in a group with a retrieval head, else the union
+// of the sets.  One warp a run.  Also clears the output (segments whose sets are
+// all empty have no slab and so no writer).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) q8_runs_kernel(const __grid_constant__ Q8AttnParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long all = (long long)p.B * p.Hkv * p.runs_stride;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)p.B * p.Hq * D; i += (long long)gridDim.x * 256)
+    store1(static_cast<T*>(p.out) + i, 0.f);
+  if (id >= (long long)p.n_run_items * 16) return;
+  int rows = 0;
+  if (id < all) {
+    const int seg = (int)(id / p.runs_stride), run = (int)(id - (long long)seg * p.runs_stride);
+    const int b = seg / p.Hkv, g = seg - b * p.Hkv, G = p.Hq / p.Hkv;
+    const int n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
+    const int base = run * kQ8Run, left = min(n - base, kQ8Run);
+    bool dense = false;
+    for (int t = 0; t < G; ++t) dense = dense || ((p.role[(g * G + t) >> 5] >> ((g * G + t) & 31)) & 1u);
+    if (left > 0) {
+      if (dense) rows = left;
+      else {
+        uint32_t u = 0;
+        const int w = (base >> 5) + lane;
+        if (lane < kQ8Run / 32 && 32 * w < n) {
+          for (int t = 0; t < G; ++t) u |= __ldcg(&p.bitmaps[((size_t)b * p.Hq + g * G + t) * p.nwords + w]);
+          if (n - 32 * w < 32) u &= (1u << (n - 32 * w)) - 1u;
+        }
+        rows = warp_sum_int(__popc(u));
+      }
+    }
+  }
+  if (lane == 0) p.run_slabs[id] = (uint8_t)((rows + 15) >> 4);
+}
+
+// ---- launches ----------------------------------------------------------------------------------
+template <typename T, int CODE, int D, int G, bool HYB>
+cudaError_t launch_g(const Q8AttnParams& p, int grid, cudaStream_t st) {
+  using C = Cfg<T, D, G>;
+  auto kfn = q8_attn_kernel<T, CODE, D, G, HYB>;
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.run([&] { return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
   if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  if ((e = launch_pdl(kfn, dim3(grid), dim3(kThreads), C::SMEM, st, p)) != cudaSuccess) return e;
+  return launch_pdl(q8_merge_kernel<T, D>, dim3(grid, G), dim3(kMergeThreads), 0, st, p);
+}
+
+template <typename T, int CODE, int D, bool HYB>
+cudaError_t launch_h(const Q8AttnParams& p, int grid, cudaStream_t st) {
+  switch (p.Hq / p.Hkv) {
+    case 1: return launch_g<T, CODE, D, 1, HYB>(p, grid, st);
+    case 2: return launch_g<T, CODE, D, 2, HYB>(p, grid, st);
+    case 4: return launch_g<T, CODE, D, 4, HYB>(p, grid, st);
+    case 8: return launch_g<T, CODE, D, 8, HYB>(p, grid, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T, int CODE, int D>
+cudaError_t launch_d(const Q8AttnParams& p, int grid, cudaStream_t st) {
+  if (!p.run_slabs) return launch_h<T, CODE, D, false>(p, grid, st);
+  const long long runs = (long long)p.n_run_items * 16;
+  if ((runs + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_pdl(q8_runs_kernel<T, D>, dim3((unsigned)((runs + 7) / 8)), dim3(256), 0, st, p);
+  return e != cudaSuccess ? e : launch_h<T, CODE, D, true>(p, grid, st);
+}
+
+template <typename T, int CODE>
+cudaError_t launch_c(const Q8AttnParams& p, int D, int grid, cudaStream_t st) {
+  return D == 128 ? launch_d<T, CODE, 128>(p, grid, st) : launch_d<T, CODE, 64>(p, grid, st);
 }
 
 }  // namespace
 
 cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms, cudaStream_t st) {
+  const int grid = std::min(sms, kQ8MaxCtas);
+  cudaError_t e;
   if (dtype == 0)
-    return code == kCodeE4M3 ? launch_c<__nv_bfloat16, kCodeE4M3>(p, D, st)
-                             : launch_c<__nv_bfloat16, kCodeInt8>(p, D, st);
-  return code == kCodeE4M3 ? launch_c<float, kCodeE4M3>(p, D, st) : launch_c<float, kCodeInt8>(p, D, st);
+    e = code == kCodeE4M3 ? launch_c<__nv_bfloat16, kCodeE4M3>(p, D, grid, st)
+                          : launch_c<__nv_bfloat16, kCodeInt8>(p, D, grid, st);
+  else
+    e = code == kCodeE4M3 ? launch_c<float, kCodeE4M3>(p, D, grid, st) : launch_c<float, kCodeInt8>(p, D, grid, st);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 }  // namespace lychee
