@@ -101,23 +101,6 @@ Layout layout_of(const lychee_shape* s) {
 size_t elem_size(const lychee_shape* s) { return s->dtype == LYCHEE_BF16 ? 2 : 4; }
 
 // ---- tensor maps for the attention kernel's row gathers -----------------------------
-// cuTensorMapEncodeTiled comes from the driver through the runtime's entry-point
-// query, so the library needs no link against libcuda.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    cudaGetLastError();
-  });
-  return fn;
-}
-
 // LYCHEE_NO_TMA_GATHER=1 in the environment (read once) makes every sparse row
 // gather of fp32 caches use 16-byte copies, the path taken when no tensor map
 // can describe the cache; for testing that path.

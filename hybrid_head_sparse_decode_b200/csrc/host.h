@@ -2,6 +2,8 @@
 // argument checks, device properties, the optional launch profiler.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -27,6 +29,24 @@ inline lychee_status check_roles(const uint8_t* role, int Hq, int* n_sparse) {
   }
   if (n_sparse) *n_sparse = ns;
   return LYCHEE_OK;
+}
+
+// ---- tensor maps ----------------------------------------------------------------
+// cuTensorMapEncodeTiled comes from the driver through the runtime's entry-point
+// query, so the library needs no link against libcuda.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    cudaGetLastError();
+  });
+  return fn;
 }
 
 // ---- device properties -----------------------------------------------------------

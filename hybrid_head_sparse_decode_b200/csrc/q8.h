@@ -57,6 +57,9 @@ struct Q8AttnParams {
   float* logits;             // [B, Hq, N_max]: raw q.k of the retrieval heads
   const int32_t* k_per_seq;  // [B] or null (checked here)
   int nwords, runs_stride, n_run_items;
+  // the cache's codes as rows of D bytes, boxes of sixteen rows, swizzled by D bytes
+  alignas(64) CUtensorMap tmk;
+  alignas(64) CUtensorMap tmv;
 };
 cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms,
                            cudaStream_t st);

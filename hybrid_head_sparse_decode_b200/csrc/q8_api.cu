@@ -100,6 +100,21 @@ lychee_status check_sets(const lychee_q8_shape* s, int k, int block) {
   return LYCHEE_OK;
 }
 
+// The codes of a cache as an array of rows of d bytes, in boxes of sixteen rows
+// whose 16-byte pieces are swizzled over 128 (d = 64: 64) bytes.  False when the
+// driver offers no encoder or refuses the map.
+bool encode_rows(CUtensorMap* m, const void* base, const lychee_q8_shape* s) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)s->d, (cuuint64_t)s->num_pages * s->Hkv * s->page};
+  const cuuint64_t strides[1] = {(cuuint64_t)s->d};
+  const cuuint32_t box[2] = {(cuuint32_t)s->d, 16u};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, s->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 Q8AttnParams attn_params(const lychee_q8_shape* s, const void* q, const lychee_q8_cache* c,
                          const int32_t* seqlens, void* out, uint32_t* err, const Q8Layout& L,
                          void* workspace) {
@@ -185,6 +200,7 @@ lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q, con
   if (sms <= 0) return LYCHEE_ERR_CUDA;
   Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);
   for (int i = 0; i < 4; ++i) p.role[i] = 0xffffffffu;
+  if (!encode_rows(&p.tmk, cache->k, s) || !encode_rows(&p.tmv, cache->v, s)) return LYCHEE_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); });
@@ -221,6 +237,7 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   p.runs_stride = L.runs_stride;
   p.n_run_items = L.n_run_items;
   fill_roles(p.role, head_role, s->Hq);
+  if (!encode_rows(&p.tmk, cache->k, s) || !encode_rows(&p.tmv, cache->v, s)) return LYCHEE_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (ns > 0) {
     // the incoming sets as bitmaps; the rows go on as they came

@@ -5,37 +5,50 @@
 // Mathematics.  With c_j, c'_j the codes of key and value j and sk, sv the scales
 // of their blocks: s_j = (q . c_j) sk / sqrt(d), p = softmax(s) over every j < n_b
 // (or over the head's set), out = sum_j p_j sv c'_j.  A sequence of no rows and an
-// empty set give zeros.  Codes become halves exactly (e4m3 and int8 both fit 11
-// bits), so both products run on the tensor cores without a second rounding of
-// the cache: q is scaled by a power of two into the halves' range (bf16 fits;
-// fp32 is held in two halves, 22 bits), q . c_j is summed in fp32 and takes the
-// scales afterwards.  The weight that multiplies the codes is w_j = p_j sv_j; it
-// is what must fit a half, so the running reference of the online softmax is the
-// maximum of s_j log2(e) + log2(sv_j), and the normaliser sums p_j beside it.
-// The reference is kept 6 below the maximum seen (weights up to 2^7) and moved
-// only when a weight would pass 2^15: weights down to 2^-31 of the largest keep
-// a place in the half's range.  With bf16 queries a weight is rounded to 11 bits
-// (the output has 8); with fp32 ones it is held in two halves.
+// empty set give zeros.  Both products run on the tensor cores without a second
+// rounding of the cache, and take the scales afterwards.
+//   q . c   bf16 queries on e4m3 codes: the codes are an operand as they are, and q
+//           is two e4m3 parts, hi = e4m3(q') and lo = e4m3(16 (q' - hi)) with q' = q
+//           times a power of two that brings its largest magnitude to [2^7, 2^8): the
+//           two hold a bf16 exactly above 2^-13 of the largest, and to 2^-21 of the
+//           largest below.  Otherwise codes become halves (exact: both code types
+//           fit 11 bits), q' has its largest magnitude in [2^13, 2^14), and fp32
+//           queries are held in two halves (22 bits).
+//   p . c'  codes become halves.  The weight that multiplies them is w_j = p_j sv_j;
+//           it is what must fit a half, so the running reference of the online
+//           softmax is the maximum of s_j log2(e) + log2(sv_j), and the normaliser
+//           sums w_j / sv_j beside it.  The reference is kept 6 below the maximum
+//           seen and moved only when a weight would pass 2^15: weights down to 2^-31
+//           of the largest keep a place in the half's range (an 8-bit float's range
+//           would lose the many small weights of a long context).  With bf16
+//           queries a weight is rounded to 11 bits (the output has 8); with fp32
+//           ones it is held in two halves.
 //
 // Work split.  The unit is a slab of 16 rows of one KV head.  All slabs of the
 // call, ordered by sequence, head and position, are cut into one equal range per
 // CTA and that into one per warp, whatever the lengths (a sequence's and a head's
 // slabs are a segment; a hybrid layer counts only the rows that some head of the
-// group uses).  A warp works alone: it copies its slabs' rows into a ring of its
-// own in shared memory (cp.async, each lane exactly the bytes it will read, so
-// the ring needs no barrier but the warp's) and runs the G heads of the group
-// over each slab at once.  At the end the CTA merges its warps' states of a
-// segment, writes what is complete and leaves at most two states open: of a
-// segment that began in an earlier CTA and of one that goes on in a later CTA.
-// The second kernel merges those.  All sums have a fixed order.
+// group uses).  A warp works alone: it brings its slabs into a ring of its own in
+// shared memory and runs the G heads of the group over each slab at once; no
+// barrier joins the warps before the end.  A full slab is 16 consecutive rows of
+// one page: two TMA boxes (K and V).  The rows of a sparse head's set, and a
+// slab cut by the sequence's end, come row by row (cp.async, absent rows as
+// zeros).  At the end the CTA merges its warps' states of a segment, writes what
+// is complete and leaves at most two states open: of a segment that began in an
+// earlier CTA and of one that goes on in a later CTA.  The second kernel merges
+// those.  When there are fewer segments than CTAs and they are short, every
+// segment is one CTA's and nothing is left to merge.  All sums have a fixed order.
 //
-// Layouts.  S = K q^T as mma.m16n8k16 with the slab's rows as M: a lane takes 16
-// consecutive bytes of rows r = lane / 4 and r + 8 (chunk lane % 4); which
-// dimension a k index means is free as long as q agrees, so its words convert to
-// A fragments in place.  O^T = V^T P with the dimensions as M: a lane takes chunk
-// lane / 4 of rows 2c, 2c + 1, 2c + 8, 2c + 9 (c = lane % 4); interleaving the
-// bytes of two rows gives the pairs along k that A wants.  P moves from the
-// accumulator layout to B by a transpose of 8x8 halves (movmatrix).
+// Layouts.  Rows lie in shared memory with the TMA's swizzle (16-byte pieces of a
+// row XORed with its number).  S = K q^T as m16n8k32 (e4m3) or m16n8k16 (halves)
+// with the slab's rows as M: a lane takes 16-byte piece c (c = lane % 4) of its
+// two rows; which dimension a k index means is free as long as q agrees, so a
+// row's words are, or convert to, A fragments in place.  O^T = V^T P with the
+// dimensions as M: a lane takes piece lane / 4 of four rows; interleaving the bytes
+// of two rows gives the pairs along k that A wants.  Which row stands at which index
+// of M and k is free too: index i is row i ^ 4 (i & 1), which makes both reads
+// free of bank conflicts.  P moves from the accumulator layout to B by a
+// transpose of 8x8 halves (movmatrix).
 #include <algorithm>
 
 #include "q8.cuh"
@@ -48,16 +61,13 @@ constexpr int kWarps = kQ8Warps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
-constexpr float kRefSlack = 14.f;    // and moves when a weight passes it by more than this
+constexpr float kRefSlack = 15.f;    // and moves when a weight passes it by more than this
+constexpr float kNoRef = -1e30f;     // no row yet (finite: differences of two stay numbers)
+constexpr uint32_t kFullSlab = 1u << 29;   // stage header: sixteen rows of one page, one scale
+constexpr uint32_t kAllHeads = 1u << 30;   // ... and every head uses every row
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async8z(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4z(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -82,9 +92,32 @@ __device__ __forceinline__ uint32_t lds_u(uint32_t a) {
 __device__ __forceinline__ void sts_u(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Rows y .. y + 15 of the map's array, all of their bytes, to dst in the map's swizzle.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar),
+      "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+               "{%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                "{%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -102,6 +135,14 @@ __device__ __forceinline__ float2 unpack_half(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// Four values -> four e4m3 codes (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
 template <typename T>
 __device__ __forceinline__ float4 load_q4(const T* p);
 template <>
@@ -117,22 +158,28 @@ __device__ __forceinline__ float4 load_q4<float>(const float* p) {
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-template <typename T, int D, int G>
+template <typename T, int CODE, int D, int G>
 struct Cfg {
+  static constexpr bool kF8 = sizeof(T) == 2 && CODE == kCodeE4M3;   // q as two e4m3 parts
   static constexpr bool kTwo = sizeof(T) == 4;           // q and the weights in two halves
   static constexpr bool kBeside = kTwo && G <= 4;        // ... in columns 0-3 and 4-7 of one product
-  static constexpr int NQ = kTwo && !kBeside ? 2 : 1;    // ... or in two products
-  static constexpr int KM = D / 16;                      // products along d (S), blocks of 16 dimensions (O)
-  static constexpr int KS = D / 32;                      // 16-byte pieces of K a lane takes of a slab
+  static constexpr int NQ = (kTwo && !kBeside) || kF8 ? 2 : 1;   // products of S per k step
+  static constexpr int KQ = kF8 ? D / 32 : D / 16;       // k steps of S
+  static constexpr int KM = D / 16;                      // blocks of 16 dimensions of O
+  static constexpr int H = D / 64;                       // 16-byte pieces of K a lane takes of a row
   static constexpr int VB = D / 8;                       // bytes of V a lane takes of each of its four rows
-  static constexpr int OFF_V = 16 * D, OFF_S = 32 * D, OFF_META = OFF_S + 128, OFF_HEAD = OFF_META + 64;
-  static constexpr int STAGE = OFF_HEAD + 16;
+  static constexpr int DATA = 32 * D;                    // a stage's rows: K, then V
+  static constexpr int OFF_V = 16 * D;
+  // beside the rows, per stage: row scales (K; log2 of V's), positions and heads, header
+  static constexpr int AUX_S = 0, AUX_META = 128, AUX_HEAD = 192, AUX = 208;
   static constexpr int LIST = kQ8Run * 2;                // a run's rows (hybrid): u16 each
-  static constexpr int WARP = kStages * STAGE + LIST;
+  static constexpr int WARP_AUX = kStages * AUX + LIST + 32;   // and the stages' mbarriers
+  static constexpr int OFF_AUX = kWarps * kStages * DATA;
   static constexpr int STATE = G * (D + 2);              // floats of a state: m[G], l[G], acc[G][D]
-  static constexpr int SMEM = kWarps * WARP;
-  static_assert(STAGE % 16 == 0 && LIST % 16 == 0, "16-byte copies");
-  static_assert(kWarps * STATE * 4 <= SMEM, "the states are merged where the rings were");
+  static constexpr int SMEM = OFF_AUX + kWarps * WARP_AUX + 1024;   // + alignment slack
+  static_assert(WARP_AUX % 16 == 0 && kStages * 8 <= 32, "aligned");
+  static_assert(DATA / 2 % 1024 == 0 || D == 64, "swizzled rows on 1024-byte (D = 64: 512-byte) boundaries");
+  static_assert(kWarps * STATE * 4 <= OFF_AUX, "the states are merged where the rings were");
 };
 
 // Where a range of slabs begins.
@@ -148,24 +195,48 @@ struct Cursor {
   int rows;             // hybrid: rows of the run
   bool packed;          // hybrid: the run's rows are consecutive
   int win;              // dense: the slab that lane 0's table entry belongs to
-  int page;             // this lane's table entry of the window / run
+  int page;             // this lane's table entry of the window / run (-1: not a page)
+  float ks, lv;         // ... and the block's scales: K's, log2 of V's
 };
 
 template <typename T, int CODE, int D, int G, bool HYB>
 struct Warp {
-  using C = Cfg<T, D, G>;
+  using C = Cfg<T, CODE, D, G>;
   const Q8AttnParams& p;
-  uint32_t ring, list;
+  uint32_t ring, aux, list, bars;
   int lane, r, c;
   Cursor cur;
+  uint32_t parity;      // bit i: the phase that stage i's mbarrier completes next
+  uint32_t gathered;    // bit i: stage i was last filled row by row
+  bool mixed;           // hybrid: the cursor's group has a sparse head
 
-  __device__ __forceinline__ Warp(const Q8AttnParams& pp, uint32_t base)
-      : p(pp), ring(base), list(base + kStages * C::STAGE) {
+  __device__ __forceinline__ Warp(const Q8AttnParams& pp, uint32_t ring_, uint32_t aux_)
+      : p(pp), ring(ring_), aux(aux_), list(aux_ + kStages * C::AUX), bars(aux_ + kStages * C::AUX + C::LIST) {
     lane = threadIdx.x & 31;
     r = lane >> 2;
     c = lane & 3;
+    parity = gathered = 0;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i)
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * i) : "memory");
+      fence_mbar_init();
+    }
+    __syncwarp();
   }
   __device__ __forceinline__ int length(int b) const { return min(max(__ldg(&p.seqlens[b]), 0), p.N_max); }
+
+  __device__ __forceinline__ bool retrieval(int h) const { return (p.role[h >> 5] >> (h & 31)) & 1u; }
+  // This lane's table entry at position `pos` (want: there is one), and its scales.
+  __device__ __forceinline__ void load_page(bool want, int pos) {
+    cur.page = want ? __ldg(&p.c.table[(size_t)cur.b * p.c.max_pages + (pos >> p.c.page_log2)]) : -1;
+    const bool ok = cur.page >= 0 && cur.page < p.c.num_pages;
+    if (want && !ok) flag_error(p.err, kErrBadIndex);
+    if (!ok) cur.page = -1;
+    const int unit = max(cur.page, 0) * p.Hkv + cur.g;
+    cur.ks = __ldg(&p.c.k_scale[unit]);
+    cur.lv = fast_log2(__ldg(&p.c.v_scale[unit]));
+  }
 
   // ---- the cursor
   __device__ __forceinline__ void enter(int seg) {
@@ -178,6 +249,9 @@ struct Warp {
     if (HYB) {
       cur.run = 0;
       cur.runs = (cur.n + kQ8Run - 1) / kQ8Run;
+      mixed = false;
+#pragma unroll
+      for (int t = 0; t < G; ++t) mixed = mixed || !retrieval(cur.g * G + t);
     } else {
       cur.count = (cur.n + 15) >> 4;
     }
@@ -217,15 +291,13 @@ struct Warp {
     const int pos0 = base + lane * 8;
     const int left = min(max(cur.n - pos0, 0), 8);
     const uint32_t in = (1u << left) - 1u;
-    const int lp = base >> p.c.page_log2;
-    const int pages = max(1, kQ8Run >> p.c.page_log2);
-    cur.page = lane < pages && lp + lane < p.c.max_pages
-                   ? __ldg(&p.c.table[(size_t)cur.b * p.c.max_pages + lp + lane]) : -1;
+    load_page(lane < (kQ8Run >> p.c.page_log2) && base + (lane << p.c.page_log2) < cur.n,
+              base + (lane << p.c.page_log2));
     uint32_t bits[G], u = 0;
 #pragma unroll
     for (int t = 0; t < G; ++t) {
       const int h = cur.g * G + t;
-      if ((p.role[h >> 5] >> (h & 31)) & 1u) bits[t] = in;
+      if (retrieval(h)) bits[t] = in;
       else {
         const int w = (base >> 5) + word;
         const uint32_t x = w < p.nwords
@@ -284,108 +356,110 @@ struct Warp {
     return enter_next();
   }
 
-  // ---- copies of the slab at the cursor into stage `st`
-  __device__ __forceinline__ void copy_rows(uint32_t st, const uint8_t* kp, const uint8_t* vp) {
-    // kp: row r's chunk c, vp: row 2c's chunk r of sixteen consecutive rows
-    const uint32_t kd = st + lane * 16;
-#pragma unroll
-    for (int j = 0; j < C::KS; ++j) {
-      constexpr int half = C::KS / 2;
-      const int row = (j / half) * 8, col = (j % half) * 64;
-      cp_async16z(kd + j * 512, kp + row * D + col, 16);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = (j >> 1) * 8 + (j & 1);
-      if (C::VB == 16) cp_async16z(st + C::OFF_V + j * 512 + lane * 16, vp + row * D, 16);
-      else cp_async8z(st + C::OFF_V + j * 256 + lane * 8, vp + row * D, 8);
-    }
-  }
-  __device__ __forceinline__ void copy_gathered(uint32_t st, uint32_t myrow, uint32_t mysize) {
-    // lane i (and i + 16) knows row i
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t row = __shfl_sync(kFull, myrow, r + 8 * i), sz = __shfl_sync(kFull, mysize, r + 8 * i);
-      const uint8_t* src = p.c.k + (size_t)row * D + 16 * c;
-#pragma unroll
-      for (int j = 0; j < C::KS / 2; ++j) cp_async16z(st + (i * (C::KS / 2) + j) * 512 + lane * 16, src + 64 * j, sz);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 2 * c + (j >> 1) * 8 + (j & 1);
-      const uint32_t row = __shfl_sync(kFull, myrow, i), sz = __shfl_sync(kFull, mysize, i);
-      const uint8_t* src = p.c.v + (size_t)row * D + C::VB * r;
-      if (C::VB == 16) cp_async16z(st + C::OFF_V + j * 512 + lane * 16, src, sz);
-      else cp_async8z(st + C::OFF_V + j * 256 + lane * 8, src, sz ? 8u : 0u);
-    }
-  }
-  __device__ __forceinline__ void copy(uint32_t st) {
+  // ---- the slab at the cursor into stage `si`
+  __device__ __forceinline__ void copy(int si) {
+    const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX;
     const int log2p = p.c.page_log2, pmask = (1 << log2p) - 1;
     const int i = lane & 15;
-    const float* scales = lane < 16 ? p.c.k_scale : p.c.v_scale;
-    uint32_t meta;
+    int e_at = 16 * cur.at + i;           // hybrid: this lane's row of the run
+    uint32_t myrow = 0, meta;
+    bool in;
+    float ks, lv;
     if (!HYB || cur.packed) {
-      // sixteen consecutive positions, all in one page (pages are whole slabs)
-      int pos0, page;
+      // consecutive positions, all in one page (pages are whole slabs)
+      int pos0, wl;
       if (HYB) {
         pos0 = cur.run * kQ8Run + 16 * cur.at;
-        page = __shfl_sync(kFull, cur.page, (16 * cur.at) >> log2p);
+        wl = (16 * cur.at) >> log2p;
       } else {
         pos0 = 16 * cur.at;
         if ((unsigned)(cur.at - cur.win) >= 32u) {
           cur.win = cur.at;
-          cur.page = cur.at + lane < cur.count
-                         ? __ldg(&p.c.table[(size_t)cur.b * p.c.max_pages + ((16 * (cur.at + lane)) >> log2p)]) : -1;
+          load_page(cur.at + lane < cur.count, 16 * (cur.at + lane));
         }
-        page = __shfl_sync(kFull, cur.page, cur.at - cur.win);
+        wl = cur.at - cur.win;
       }
-      const int rows = min(16, cur.n - pos0);
-      const bool ok = page >= 0 && page < p.c.num_pages;
-      if (!ok && lane == 0) flag_error(p.err, kErrBadIndex);
-      const int unit = (ok ? page : 0) * p.Hkv + cur.g;
-      const uint32_t row0 = ((uint32_t)unit << log2p) + (pos0 & pmask);
-      if (ok && rows == 16) {
-        copy_rows(st, p.c.k + (size_t)row0 * D + r * D + 16 * c, p.c.v + (size_t)row0 * D + 2 * c * D + C::VB * r);
-      } else {
-        const bool in = ok && i < rows;
-        copy_gathered(st, row0 + (in ? i : 0), in ? 16u : 0u);
-      }
-      cp_async4z(st + C::OFF_S + lane * 4, scales + unit, ok ? 4u : 0u);
-      uint32_t heads = (1u << G) - 1u;
-      if (HYB && i < rows) {
+      const int page = __shfl_sync(kFull, cur.page, wl);
+      ks = __shfl_sync(kFull, cur.ks, wl);
+      lv = __shfl_sync(kFull, cur.lv, wl);
+      const uint32_t row0 = ((uint32_t)(page * p.Hkv + cur.g) << log2p) + (pos0 & pmask);
+      uint32_t heads = 0xffu;
+      if (HYB && mixed && e_at < cur.rows) {
         uint16_t e;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * (16 * cur.at + i)));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * e_at));
         heads = e >> 8;
       }
-      meta = (uint32_t)(pos0 + i) | (ok && i < rows ? heads << 24 : 0u);
+      if (page >= 0 && cur.n - pos0 >= 16) {
+        if (HYB && mixed && lane < 16) sts_u(ax + C::AUX_META + lane * 4, heads << 24);
+        if (lane == 0) {
+          const uint32_t bar = bars + 8 * si;
+          if ((gathered >> si) & 1u) fence_proxy_async_smem();   // ordinary writes before the TMA's
+          asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((uint32_t)C::DATA)
+                       : "memory");
+          const uint64_t policy = l2_evict_first_policy();
+          tma_rows(st, &p.tmk, (int)row0, bar, policy);
+          tma_rows(st + C::OFF_V, &p.tmv, (int)row0, bar, policy);
+          sts128(ax + C::AUX_HEAD, (uint32_t)cur.seg, (uint32_t)pos0 | kFullSlab | (HYB && mixed ? 0u : kAllHeads),
+                 __float_as_uint(ks), __float_as_uint(lv));
+        }
+        gathered &= ~(1u << si);
+        return;
+      }
+      in = page >= 0 && i < cur.n - pos0;
+      myrow = row0 + i;
+      meta = in ? heads << 24 : 0u;
+      if (HYB) meta |= (uint32_t)(pos0 + i);
     } else {
-      const int e_at = 16 * cur.at + i;
       uint16_t e = 0;
       if (e_at < cur.rows) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * e_at));
-      const int off = e & 255;
-      const int page = __shfl_sync(kFull, cur.page, off >> log2p);
-      const bool in = e_at < cur.rows, ok = page >= 0 && page < p.c.num_pages;
-      if (in && !ok) flag_error(p.err, kErrBadIndex);
-      const int unit = (ok ? page : 0) * p.Hkv + cur.g;
-      const int pos = cur.run * kQ8Run + off;
-      copy_gathered(st, ((uint32_t)unit << log2p) + (pos & pmask), in && ok ? 16u : 0u);
-      cp_async4z(st + C::OFF_S + lane * 4, scales + unit, in && ok ? 4u : 0u);
-      meta = (uint32_t)pos | (in && ok ? (uint32_t)(e >> 8) << 24 : 0u);
+      const int off = e & 255, wl = off >> log2p;
+      const int page = __shfl_sync(kFull, cur.page, wl);
+      ks = __shfl_sync(kFull, cur.ks, wl);
+      lv = __shfl_sync(kFull, cur.lv, wl);
+      in = e_at < cur.rows && page >= 0;
+      myrow = ((uint32_t)(page * p.Hkv + cur.g) << log2p) + (off & pmask);   // (a run begins on a page)
+      meta = in ? (uint32_t)(e >> 8) << 24 : 0u;
     }
-    if (lane < 16) sts_u(st + C::OFF_META + lane * 4, meta);
-    if (lane == 16) sts_u(st + C::OFF_HEAD, (uint32_t)cur.seg);
+    // row by row; lane i (and i + 16) knows row i.  An absent row is zeros with scale 1.
+    gathered |= 1u << si;
+    if (!in) myrow = 0xffffffffu;
+    constexpr int LPR = D / 16, RPI = 32 / LPR;   // lanes a row, rows an instruction
+    const int lr = lane / LPR, q = lane % LPR;
+#pragma unroll
+    for (int j = 0; j < 16 / RPI; ++j) {
+      const int R = RPI * j + lr;
+      const uint32_t row = __shfl_sync(kFull, myrow, R);
+      const bool have = row != 0xffffffffu;
+      const size_t at = have ? (size_t)row * D + 16 * q : 0;
+      const uint32_t dst = st + R * D + ((D == 128 ? q ^ (R & 7) : q ^ ((R >> 1) & 3)) << 4);
+      cp_async16z(dst, p.c.k + at, have ? 16u : 0u);
+      cp_async16z(dst + C::OFF_V, p.c.v + at, have ? 16u : 0u);
+    }
+    sts_u(ax + C::AUX_S + lane * 4, __float_as_uint(!in ? (lane < 16 ? 1.f : 0.f) : lane < 16 ? ks : lv));
+    if (lane < 16) sts_u(ax + C::AUX_META + lane * 4, meta);
+    if (lane == 0) sts128(ax + C::AUX_HEAD, (uint32_t)cur.seg, 0u, 0u, 0u);
   }
 
   // ---- the heads' states
-  uint32_t qf[C::NQ][C::KM][2];   // q as B fragments
+  uint32_t qf[C::NQ][C::KQ][2];   // q as B fragments
   float fq[2];                    // powers of two that undo q's scaling, of this lane's two columns
-  float ref[2], l[2];             // reference (log2) and sum of weights, of this lane's two columns
+  float ref[2], l[2];             // reference (log2) and sum of p, of this lane's two columns
   float acc[C::KM][4];
 
   __device__ __forceinline__ int column_head(int j) const { return (C::kBeside ? 2 * (c & 1) : 2 * c) + j; }
 
+  size_t logit_row;               // hybrid: where this lane's first column's logits go
+  int logit_cols;                 // ... bit j: column j is a retrieval head (written by this lane)
+
   __device__ __forceinline__ void load_q(int seg) {
     const int b = seg / p.Hkv, g = seg - b * p.Hkv;
+    if (HYB) {
+      logit_row = ((size_t)b * p.Hq + g * G + column_head(0)) * p.N_max;
+      logit_cols = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (column_head(j) < G && (!C::kBeside || c < 2) && retrieval(g * G + column_head(j))) logit_cols |= 1 << j;
+    }
     const int t = C::kBeside ? r & 3 : r;
     float4 x[C::KM];
     float mx = 0.f;
@@ -399,19 +473,33 @@ struct Warp {
     }
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    // the largest magnitude to [2^13, 2^14) (below 2^-100 the same factor as at 2^-100)
+    // the largest magnitude to [2^top, 2^(top + 1)) (below 2^-100 the same factor as at 2^-100)
+    constexpr int top = C::kF8 ? 7 : 13;
     const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
-    const float up = exp2_int(13 - e), down = exp2_int(e - 13);
+    const float up = exp2_int(top - e);
+    const float down = mx < INFINITY ? exp2_int(e - top) : NAN;   // (an infinite q has no score)
+    if constexpr (C::kF8) {
+      // x[m] holds four dimensions: two m to a k step of 32
+#pragma unroll
+      for (int m = 0; m < C::KM; ++m) {
+        const float a[4] = {x[m].x * up, x[m].y * up, x[m].z * up, x[m].w * up};
+        const uint32_t hi = e4m3x4(a[0], a[1], a[2], a[3]);
+        const float4 h = codes_to_float<kCodeE4M3>(hi);
+        qf[0][m >> 1][m & 1] = hi;
+        qf[C::NQ - 1][m >> 1][m & 1] =
+            e4m3x4(16.f * (a[0] - h.x), 16.f * (a[1] - h.y), 16.f * (a[2] - h.z), 16.f * (a[3] - h.w));
+      }
+    } else {
 #pragma unroll
     for (int m = 0; m < C::KM; ++m) {
       const float a = x[m].x * up, bb = x[m].y * up, cc = x[m].z * up, d = x[m].w * up;
       uint32_t w0 = pack_half(a, bb), w1 = pack_half(cc, d);
-      if (C::kTwo) {
+      if constexpr (C::kTwo) {
         const float2 h0 = unpack_half(w0), h1 = unpack_half(w1);
         const uint32_t l0 = pack_half(a - h0.x, bb - h0.y), l1 = pack_half(cc - h1.x, d - h1.y);
-        if (C::NQ == 2) {
-          qf[C::NQ - 1][m][0] = l0;
-          qf[C::NQ - 1][m][1] = l1;
+        if constexpr (C::NQ == 2) {
+          qf[1][m][0] = l0;
+          qf[1][m][1] = l1;
         } else if (r >= 4) {
           w0 = l0;
           w1 = l1;
@@ -420,26 +508,36 @@ struct Warp {
       qf[0][m][0] = w0;
       qf[0][m][1] = w1;
     }
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) fq[j] = __shfl_sync(kFull, down, (column_head(j) & 7) * 4);
   }
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int m = 0; m < C::KM; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
-    ref[0] = ref[1] = -INFINITY;
+    ref[0] = ref[1] = kNoRef;
     l[0] = l[1] = 0.f;
   }
 
-  // ---- one slab
-  __device__ __forceinline__ void consume(uint32_t st, int seg) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-      float s2[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t ks = st + lane * 16;
+  // ---- one slab: stage `si`, its header in hd
+  __device__ __forceinline__ void consume(int si, uint4 hd, int seg) {
+    const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX;
+    const int R = r ^ ((r & 1) << 2);      // this lane's rows of S: R and R + 8
+    // ---- S
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t ka = st + R * D + ((D == 128 ? c ^ (R & 7) : c ^ ((R >> 1) & 3)) << 4);
 #pragma unroll
-      for (int h = 0; h < C::KS / 2; ++h) {
-        const uint4 lo = lds128(ks + h * 512), hi = lds128(ks + (C::KS / 2 + h) * 512);
-        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    for (int h = 0; h < C::H; ++h) {
+      const uint4 lo = lds128(ka ^ (h << 6)), hi = lds128((ka ^ (h << 6)) + 8 * D);
+      const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+      if constexpr (C::kF8) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int m = h * 2 + j;
+          mma_e4m3(s, wl[2 * j], wh[2 * j], wl[2 * j + 1], wh[2 * j + 1], qf[0][m][0], qf[0][m][1]);
+          mma_e4m3(s2, wl[2 * j], wh[2 * j], wl[2 * j + 1], wh[2 * j + 1], qf[C::NQ - 1][m][0], qf[C::NQ - 1][m][1]);
+        }
+      } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int m = h * 4 + j;
@@ -447,56 +545,63 @@ struct Warp {
           codes_to_half<CODE>(wl[j], a0, a2);
           codes_to_half<CODE>(wh[j], a1, a3);
           mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[0][m][0], qf[0][m][1]);
-          if (C::NQ == 2) mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[C::NQ - 1][m][0], qf[C::NQ - 1][m][1]);
+          if constexpr (C::NQ == 2) mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[C::NQ - 1][m][0], qf[C::NQ - 1][m][1]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += s2[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = C::kF8 ? fmaf(s2[i], 0.0625f, s[i]) : s[i] + s2[i];
     if (C::kBeside) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(kFull, s[i], 2);
     }
-    // s[0], s[1]: row r, columns 2c and 2c + 1; s[2], s[3]: row r + 8
-    float w[4], t[4];
-    float sv[2];
-    bool on[4];
+    // s[0], s[1]: row R, columns 2c and 2c + 1; s[2], s[3]: row R + 8
+    const bool full = hd.y & kFullSlab;
+    float sk[2] = {__uint_as_float(hd.z), __uint_as_float(hd.z)}, lv[2] = {__uint_as_float(hd.w), __uint_as_float(hd.w)};
+    uint32_t meta[2] = {0xff000000u, 0xff000000u};
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sk[i] = lds_f(ax + C::AUX_S + (R + 8 * i) * 4);
+        lv[i] = lds_f(ax + C::AUX_S + (16 + R + 8 * i) * 4);
+        meta[i] = lds_u(ax + C::AUX_META + (R + 8 * i) * 4);
+      }
+    } else if (HYB && !(hd.y & kAllHeads)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) meta[i] = lds_u(ax + C::AUX_META + (R + 8 * i) * 4);
+    }
+    // t: log2 of a row's weight times its scale, -inf where a head does not use it.
+    // (Columns beyond the group's heads hold zero queries; nothing reads them.)
+    float t[4];
     bool over = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float sk = lds_f(st + C::OFF_S + (r + 8 * i) * 4);
-      sv[i] = lds_f(st + C::OFF_S + (16 + r + 8 * i) * 4);
-      const uint32_t meta = lds_u(st + C::OFF_META + (r + 8 * i) * 4);
-      const float ev = (float)((int)((__float_as_uint(sv[i]) >> 23) & 255u) - 127);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        const float raw = s[2 * i + j] * (sk[i] * fq[j]);
         const int h = column_head(j);
-        const float raw = s[2 * i + j] * sk * fq[j];
-        on[2 * i + j] = h < G && ((meta >> (24 + (h & 7))) & 1u);
-        if (HYB && h < G && p.logits && (!C::kBeside || c < 2)) {
-          const int b = seg / p.Hkv, hq = (seg - b * p.Hkv) * G + h;
-          if (on[2 * i + j] && ((p.role[hq >> 5] >> (hq & 31)) & 1u))
-            p.logits[((size_t)b * p.Hq + hq) * p.N_max + (meta & 0xffffffu)] = raw;
+        if (HYB) {
+          const bool on = (meta[i] >> (24 + (h & 7))) & 1u;
+          if (on && ((logit_cols >> j) & 1)) {
+            const int pos = full ? (int)(hd.y & 0xffffffu) + R + 8 * i : (int)(meta[i] & 0xffffffu);
+            p.logits[logit_row + (size_t)j * p.N_max + pos] = raw;
+          }
+          t[2 * i + j] = on ? fmaf(raw, p.scale_log2, lv[i]) : -INFINITY;
+        } else {
+          t[2 * i + j] = meta[i] ? fmaf(raw, p.scale_log2, lv[i]) : -INFINITY;
         }
-        t[2 * i + j] = raw * p.scale_log2;
-        over = over || (on[2 * i + j] && t[2 * i + j] + ev > ref[j] + kRefSlack);
+        over = over || t[2 * i + j] > ref[j] + kRefSlack;
       }
-    }
     if (__any_sync(kFull, over)) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float ev = (float)((int)((__float_as_uint(sv[i]) >> 23) & 255u) - 127);
-          if (on[2 * i + j]) mx = fmaxf(mx, t[2 * i + j] + ev);
-        }
+        float mx = fmaxf(t[j], t[2 + j]);
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
         if (mx > ref[j] + kRefSlack) {
           const float to = mx - kRefBelow;
-          const float f = fast_exp2(ref[j] - to);   // 0 while the reference is -inf
+          const float f = fast_exp2(ref[j] - to);   // 0 from kNoRef
           l[j] *= f;
 #pragma unroll
           for (int m = 0; m < C::KM; ++m) {
@@ -507,35 +612,41 @@ struct Warp {
         }
       }
     }
+    // weights, and their sums without the scales
+    float w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      const float inv = fast_exp2(-lv[i]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float e = on[2 * i + j] ? fast_exp2(t[2 * i + j] - ref[j]) : 0.f;
-        l[j] += e;
-        w[2 * i + j] = on[2 * i + j] ? e * sv[i] : 0.f;
+        w[2 * i + j] = fast_exp2(t[2 * i + j] - ref[j]);
+        l[j] = fmaf(w[2 * i + j], inv, l[j]);
       }
-    uint32_t pb[C::NQ][2];
+    }
+    uint32_t pb[C::kTwo && !C::kBeside ? 2 : 1][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
-      if (C::kTwo) {
+      if constexpr (C::kTwo) {
         const float2 hf = unpack_half(hi);
         const uint32_t lo = pack_half(w[2 * i] - hf.x, w[2 * i + 1] - hf.y);
-        if (C::NQ == 2) pb[C::NQ - 1][i] = movmatrix_trans(lo);
+        if constexpr (!C::kBeside) pb[1][i] = movmatrix_trans(lo);
         else if (c >= 2) hi = lo;
       }
       pb[0][i] = movmatrix_trans(hi);
     }
-    // the values: words of rows 2c, 2c + 1, 2c + 8, 2c + 9
+    // ---- O: rows Ra, Rb (k indices 2c, 2c + 1), Ra + 8, Rb + 8
+    const int Ra = 2 * c, Rb = (2 * c) ^ 5;
+    const uint32_t vs = st + C::OFF_V;
     uint32_t v[4][C::VB / 4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if constexpr (C::VB == 16) {
-        const uint4 x = lds128(st + C::OFF_V + j * 512 + lane * 16);
+      const int Rv = (j & 1) ? Rb : Ra;
+      if constexpr (D == 128) {
+        const uint4 x = lds128(vs + Rv * D + ((r ^ (Rv & 7)) << 4) + (j >> 1) * 8 * D);
         v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
       } else {
-        const uint2 x = lds64(st + C::OFF_V + j * 256 + lane * 8);
+        const uint2 x = lds64(vs + Rv * D + (((r >> 1) ^ ((Rv >> 1) & 3)) << 4) + (r & 1) * 8 + (j >> 1) * 8 * D);
         v[j][0] = x.x; v[j][1] = x.y;
       }
     }
@@ -548,7 +659,7 @@ struct Warp {
         codes_to_half<CODE>(__byte_perm(v[0][k], v[1][k], sel), a0, a1);
         codes_to_half<CODE>(__byte_perm(v[2][k], v[3][k], sel), a2, a3);
         mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[0][0], pb[0][1]);
-        if (C::NQ == 2) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[C::NQ - 1][0], pb[C::NQ - 1][1]);
+        if constexpr (C::kTwo && !C::kBeside) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[1][0], pb[1][1]);
       }
     }
   }
@@ -613,11 +724,10 @@ struct WarpEnd {
 // One merged column over a chain of states.
 struct Chain {
   float m, l, a;
-  __device__ __forceinline__ void clear() { m = -INFINITY; l = 0.f; a = 0.f; }
+  __device__ __forceinline__ void clear() { m = kNoRef; l = 0.f; a = 0.f; }
   __device__ __forceinline__ void add(float m2, float l2, float a2) {
-    if (m2 == -INFINITY) return;
     const float M = fmaxf(m, m2);
-    const float f = m == -INFINITY ? 0.f : fast_exp2(m - M), f2 = fast_exp2(m2 - M);
+    const float f = fast_exp2(m - M), f2 = fast_exp2(m2 - M);
     l = l * f + l2 * f2;
     a = a * f + a2 * f2;
     m = M;
@@ -645,8 +755,9 @@ __device__ __forceinline__ long long item_slabs(const Q8AttnParams& p, int i, in
 
 template <typename T, int CODE, int D, int G, bool HYB>
 __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
-  using C = Cfg<T, D, G>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  using C = Cfg<T, CODE, D, G>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ long long s_wsum[kWarps];
   __shared__ Start s_start[kWarps];
   __shared__ WarpEnd s_end[kWarps];
@@ -655,6 +766,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   pdl_wait();
 
   // ---- how many slabs there are, and where each warp's begin
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.B; b += kThreads) {
+      const int n = __ldg(&p.seqlens[b]);
+      if (n < 0 || n > p.N_max) flag_error(p.err, kErrBadSeqlen);
+      if (HYB && p.k_per_seq && n > 0 && __ldg(&p.k_per_seq[b]) < 1) flag_error(p.err, kErrBadBudget);
+    }
   const int n_items = HYB ? p.n_run_items : p.B;
   long long total = 0;
   {
@@ -668,12 +785,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     for (int w = 0; w < kWarps; ++w) total += s_wsum[w];
     __syncthreads();
   }
-  if (blockIdx.x == 0)
-    for (int b = tid; b < p.B; b += kThreads) {
-      const int n = __ldg(&p.seqlens[b]);
-      if (n < 0 || n > p.N_max) flag_error(p.err, kErrBadSeqlen);
-      if (HYB && p.k_per_seq && n > 0 && __ldg(&p.k_per_seq[b]) < 1) flag_error(p.err, kErrBadBudget);
-    }
   if (!HYB) {
     // sequences of no rows give zeros
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)
@@ -735,10 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   }
 
   // ---- the warp's slabs
-  const uint32_t base = smem_u32(smem) + warp * C::WARP;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * C::DATA;
   WarpEnd end{-1, -1, 0};
   float* scratch = p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE;
-  Warp<T, CODE, D, G, HYB> wk(p, base);
+  Warp<T, CODE, D, G, HYB> wk(p, ring, smem_u32(smem) + C::OFF_AUX + warp * C::WARP_AUX);
   if (mine > 0) {
     const Start s0 = s_start[warp];
     wk.begin(s0);
@@ -750,42 +861,44 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     for (int i = 0; i < kStages - 1; ++i) {
       if (copied > 0 && copied < mine && !wk.advance()) mine = copied;
       if (copied < mine) {
-        wk.copy(base + i * C::STAGE);
+        wk.copy(i);
         ++copied;
       }
       cp_async_commit();
     }
-    int seg = -1;
-    uint32_t st = base, st_in = base + (kStages - 1) * C::STAGE;
-    const uint32_t ring_end = base + kStages * C::STAGE;
+    int seg = s0.seg;
+    wk.load_q(seg);
+    wk.reset();
+    int si = 0, so = kStages - 1;     // the stage read next, the stage filled next
     for (int i = 0; i < mine; ++i) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      const int now = (int)lds_u(st + C::OFF_HEAD);
-      if (now != seg) {
-        if (seg >= 0) {
-          if (began) wk.write_out(seg);
-          else {
-            wk.write_state(scratch);
-            end.ended = seg;
-          }
-          began = true;
+      const uint4 hd = lds128(wk.aux + si * C::AUX + C::AUX_HEAD);
+      if (hd.y & kFullSlab) {
+        uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX + C::LIST) + si;
+        if (!mbar_wait(bar, (wk.parity >> si) & 1u, p.err)) break;   // (flagged; the result is lost)
+        wk.parity ^= 1u << si;
+      }
+      if ((int)hd.x != seg) {
+        if (began) wk.write_out(seg);
+        else {
+          wk.write_state(scratch);
+          end.ended = seg;
         }
-        seg = now;
+        began = true;
+        seg = (int)hd.x;
         wk.load_q(seg);
         wk.reset();
       }
       if (copied < mine && !wk.advance()) mine = copied;
       if (copied < mine) {
-        wk.copy(st_in);
+        wk.copy(so);
         ++copied;
       }
       cp_async_commit();
-      wk.consume(st, seg);
-      st += C::STAGE;
-      if (st == ring_end) st = base;
-      st_in += C::STAGE;
-      if (st_in == ring_end) st_in = base;
+      wk.consume(si, hd, seg);
+      si = si + 1 == kStages ? 0 : si + 1;
+      so = so + 1 == kStages ? 0 : so + 1;
       __syncwarp();   // the stage is free to be written
     }
     // is the last segment complete?  (the cursor stands on its last copied slab)
@@ -954,7 +1067,7 @@ __global__ void __launch_bounds__(256) q8_runs_kernel(const __grid_constant__ Q8
 // ---- launches ----------------------------------------------------------------------------------
 template <typename T, int CODE, int D, int G, bool HYB>
 cudaError_t launch_g(const Q8AttnParams& p, int grid, cudaStream_t st) {
-  using C = Cfg<T, D, G>;
+  using C = Cfg<T, CODE, D, G>;
   auto kfn = q8_attn_kernel<T, CODE, D, G, HYB>;
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.run([&] { return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
