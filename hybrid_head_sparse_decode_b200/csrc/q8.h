@@ -37,6 +37,7 @@ cudaError_t launch_q8_append(const Q8AppendParams& p, int dtype, int code, int D
 constexpr int kQ8Warps = 16;       // warps of an attention CTA (one CTA an SM)
 constexpr int kQ8MaxCtas = 160;    // attention CTAs at most (the workspace holds that many states)
 constexpr int kQ8MinSlabs = 2;     // slabs of 16 rows a warp takes at least, while there are any
+constexpr int kQ8WholeMax = 1024;  // positions of a segment that one CTA takes alone, at most
 constexpr int kQ8Run = 256;        // positions of a run (hybrid: the unit whose rows are listed)
 struct Q8AttnParams {
   Q8Cache c;
@@ -57,6 +58,7 @@ struct Q8AttnParams {
   float* logits;             // [B, Hq, N_max]: raw q.k of the retrieval heads
   const int32_t* k_per_seq;  // [B] or null (checked here)
   int nwords, runs_stride, n_run_items;
+  int whole;                 // 1: CTA x takes segment x whole, nothing is left open
   // the cache's codes as rows of D bytes, boxes of sixteen rows, swizzled by D bytes
   alignas(64) CUtensorMap tmk;
   alignas(64) CUtensorMap tmv;

@@ -380,28 +380,30 @@ struct Warp {
         wl = cur.at - cur.win;
       }
       const int page = __shfl_sync(kFull, cur.page, wl);
+      const uint32_t row0 = ((uint32_t)(page * p.Hkv + cur.g) << log2p) + (pos0 & pmask);
+      const bool full = page >= 0 && cur.n - pos0 >= 16;
+      if (full && lane == 0) {
+        const uint32_t bar = bars + 8 * si;
+        if ((gathered >> si) & 1u) fence_proxy_async_smem();   // ordinary writes before the TMA's
+        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((uint32_t)C::DATA)
+                     : "memory");
+        const uint64_t policy = l2_evict_first_policy();
+        tma_rows(st, &p.tmk, (int)row0, bar, policy);
+        tma_rows(st + C::OFF_V, &p.tmv, (int)row0, bar, policy);
+      }
       ks = __shfl_sync(kFull, cur.ks, wl);
       lv = __shfl_sync(kFull, cur.lv, wl);
-      const uint32_t row0 = ((uint32_t)(page * p.Hkv + cur.g) << log2p) + (pos0 & pmask);
       uint32_t heads = 0xffu;
       if (HYB && mixed && e_at < cur.rows) {
         uint16_t e;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * e_at));
         heads = e >> 8;
       }
-      if (page >= 0 && cur.n - pos0 >= 16) {
+      if (full) {
         if (HYB && mixed && lane < 16) sts_u(ax + C::AUX_META + lane * 4, heads << 24);
-        if (lane == 0) {
-          const uint32_t bar = bars + 8 * si;
-          if ((gathered >> si) & 1u) fence_proxy_async_smem();   // ordinary writes before the TMA's
-          asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((uint32_t)C::DATA)
-                       : "memory");
-          const uint64_t policy = l2_evict_first_policy();
-          tma_rows(st, &p.tmk, (int)row0, bar, policy);
-          tma_rows(st + C::OFF_V, &p.tmv, (int)row0, bar, policy);
+        if (lane == 0)
           sts128(ax + C::AUX_HEAD, (uint32_t)cur.seg, (uint32_t)pos0 | kFullSlab | (HYB && mixed ? 0u : kAllHeads),
                  __float_as_uint(ks), __float_as_uint(lv));
-        }
         gathered &= ~(1u << si);
         return;
       }
@@ -451,26 +453,34 @@ struct Warp {
   size_t logit_row;               // hybrid: where this lane's first column's logits go
   int logit_cols;                 // ... bit j: column j is a retrieval head (written by this lane)
 
-  __device__ __forceinline__ void load_q(int seg) {
+  struct RawQ {
+    float4 x[C::KM];
+  };
+  __device__ __forceinline__ void fetch_q(int seg, RawQ& raw) const {
     const int b = seg / p.Hkv, g = seg - b * p.Hkv;
+    const int t = C::kBeside ? r & 3 : r;
+#pragma unroll
+    for (int m = 0; m < C::KM; ++m) {
+      raw.x[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < G)
+        raw.x[m] = load_q4<T>(static_cast<const T*>(p.q) + ((size_t)b * p.Hq + g * G + t) * D + (m >> 2) * 64 +
+                              16 * c + 4 * (m & 3));
+    }
+  }
+  __device__ __forceinline__ void set_q(int seg, const RawQ& q) {
     if (HYB) {
+      const int b = seg / p.Hkv, g = seg - b * p.Hkv;
       logit_row = ((size_t)b * p.Hq + g * G + column_head(0)) * p.N_max;
       logit_cols = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (column_head(j) < G && (!C::kBeside || c < 2) && retrieval(g * G + column_head(j))) logit_cols |= 1 << j;
     }
-    const int t = C::kBeside ? r & 3 : r;
-    float4 x[C::KM];
+    const float4 (&x)[C::KM] = q.x;
     float mx = 0.f;
 #pragma unroll
-    for (int m = 0; m < C::KM; ++m) {
-      x[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < G)
-        x[m] = load_q4<T>(static_cast<const T*>(p.q) + ((size_t)b * p.Hq + g * G + t) * D + (m >> 2) * 64 +
-                          16 * c + 4 * (m & 3));
+    for (int m = 0; m < C::KM; ++m)
       mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x[m].x), fabsf(x[m].y)), fmaxf(fabsf(x[m].z), fabsf(x[m].w))));
-    }
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
     // the largest magnitude to [2^top, 2^(top + 1)) (below 2^-100 the same factor as at 2^-100)
@@ -740,17 +750,57 @@ __device__ __forceinline__ int warp_sum_int(int v) {
   return v;
 }
 
-// Slabs of item i: of sequence i over all its KV heads (dense), of run i (hybrid;
-// sixteen runs to an item).
+// What the ranges are counted in: sequences (dense: the slabs of all their KV
+// heads), or sixteen runs (hybrid).
+struct Item {
+  uint4 runs;           // hybrid: the slab counts, a byte each
+  long long slabs;
+};
 template <bool HYB>
-__device__ __forceinline__ long long item_slabs(const Q8AttnParams& p, int i, int n_items) {
-  if (i >= n_items) return 0;
+__device__ __forceinline__ Item load_item(const Q8AttnParams& p, int i, int n_items) {
+  Item it{make_uint4(0u, 0u, 0u, 0u), 0};
+  if (i >= n_items) return it;
   if (HYB) {
     const uint4 x = __ldcg(reinterpret_cast<const uint4*>(p.run_slabs) + i);
-    return (long long)__dp4a(x.x, 0x01010101u, __dp4a(x.y, 0x01010101u, __dp4a(x.z, 0x01010101u, __dp4a(x.w, 0x01010101u, 0u))));
+    it.runs = x;
+    it.slabs = (long long)__dp4a(
+        x.x, 0x01010101u, __dp4a(x.y, 0x01010101u, __dp4a(x.z, 0x01010101u, __dp4a(x.w, 0x01010101u, 0u))));
+  } else {
+    const int n = min(max(__ldg(&p.seqlens[i]), 0), p.N_max);
+    it.slabs = (long long)((n + 15) >> 4) * p.Hkv;
   }
-  const int n = min(max(__ldg(&p.seqlens[i]), 0), p.N_max);
-  return (long long)((n + 15) >> 4) * p.Hkv;
+  return it;
+}
+// Slab `rel` of item i.
+template <bool HYB>
+__device__ __forceinline__ Start start_at(const Q8AttnParams& p, const Item& it, int i, int rel) {
+  Start s;
+  if (HYB) {
+    const uint32_t w[4] = {it.runs.x, it.runs.y, it.runs.z, it.runs.w};
+    int at = 0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int k = (int)((w[j >> 2] >> (8 * (j & 3))) & 255u);
+      if (!found) {
+        if (rel < k) found = true;
+        else {
+          rel -= k;
+          at = min(at + 1, 15);
+        }
+      }
+    }
+    const int run = i * 16 + at;
+    s.seg = run / p.runs_stride;
+    s.run = run - s.seg * p.runs_stride;
+    s.slab = rel;
+  } else {
+    const int len = (int)it.slabs / p.Hkv;
+    s.seg = i * p.Hkv + rel / len;
+    s.run = 0;
+    s.slab = rel % len;
+  }
+  return s;
 }
 
 template <typename T, int CODE, int D, int G, bool HYB>
@@ -761,8 +811,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   __shared__ long long s_wsum[kWarps];
   __shared__ Start s_start[kWarps];
   __shared__ WarpEnd s_end[kWarps];
+  __shared__ int s_has[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmk)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmv)) : "memory");
+  }
   pdl_wait();
 
   // ---- how many slabs there are, and where each warp's begin
@@ -773,17 +828,97 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       if (HYB && p.k_per_seq && n > 0 && __ldg(&p.k_per_seq[b]) < 1) flag_error(p.err, kErrBadBudget);
     }
   const int n_items = HYB ? p.n_run_items : p.B;
-  long long total = 0;
-  {
-    long long mine = 0;
-    for (int i = tid; i < n_items; i += kThreads) mine += item_slabs<HYB>(p, i, n_items);
+  Start s0{0, 0, 0};
+  int mine = 0;
+  // the ranges of [0, total): per CTA, at least kQ8MinSlabs a warp, then per warp
+  long long c0 = 0, c1 = 0, per_warp = 1;
+  auto cut_ranges = [&](long long total) {
+    const long long per_cta = max((total + gridDim.x - 1) / gridDim.x, (long long)kQ8MinSlabs * kWarps);
+    c0 = min(total, per_cta * blockIdx.x);
+    c1 = min(total, c0 + per_cta);
+    per_warp = max((c1 - c0 + kWarps - 1) / kWarps, 1LL);
+    const long long w0 = min(c1, c0 + per_warp * warp);
+    mine = (int)(min(c1, w0 + per_warp) - w0);
+  };
+  // the warps whose ranges begin in [lo, lo + it.slabs)
+  auto place = [&](const Item& it, int i, long long lo) {
+    const long long hi = lo + it.slabs;
+    if (it.slabs > 0 && hi > c0 && lo < c1) {
+      int w = lo > c0 ? (int)((lo - c0 + per_warp - 1) / per_warp) : 0;
+      for (; w < kWarps && c0 + w * per_warp < min(hi, c1); ++w)
+        s_start[w] = start_at<HYB>(p, it, i, (int)(c0 + w * per_warp - lo));
+    }
+  };
+  // exclusive prefix of v over the CTA's threads; `sum` gets the total
+  auto scan = [&](long long v, long long& sum) {
+    long long incl = v;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
-    if (lane == 0) s_wsum[warp] = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
     __syncthreads();
+    long long off = 0;
+    sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_wsum[w];
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) off += s_wsum[w];
+      sum += s_wsum[w];
+    }
+    return off + incl - v;
+  };
+  if (p.whole) {
+    // segment blockIdx.x is this CTA's
+    if ((int)blockIdx.x < p.B * p.Hkv) {
+      int k = 0, runs = 0;   // hybrid: this lane's run (there are at most 32), the runs before it
+      int total;
+      if (HYB) {
+        if (lane < p.runs_stride) k = __ldcg(&p.run_slabs[(size_t)blockIdx.x * p.runs_stride + lane]);
+        runs = k;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, runs, o);
+          if (lane >= o) runs += y;
+        }
+        total = __shfl_sync(kFull, runs, 31);
+      } else {
+        total = (min(max(__ldg(&p.seqlens[blockIdx.x / p.Hkv]), 0), p.N_max) + 15) >> 4;
+      }
+      const int per = (total + kWarps - 1) / kWarps, w0 = min(total, per * warp);
+      mine = min(total, w0 + per) - w0;
+      s0.seg = blockIdx.x;
+      s0.slab = w0;
+      if (HYB) {
+        const uint32_t in = __ballot_sync(kFull, w0 < runs);   // the first lane: the run of slab w0
+        s0.run = in ? __ffs(in) - 1 : 0;
+        s0.slab = w0 - (__shfl_sync(kFull, runs - k, s0.run));
+      }
+    }
+  } else if (n_items <= kThreads) {
+    const Item it = load_item<HYB>(p, tid, n_items);
+    long long total;
+    const long long lo = scan(it.slabs, total);
+    cut_ranges(total);
+    place(it, tid, lo);
     __syncthreads();
+    s0 = s_start[warp];
+  } else {
+    long long mine_all = 0, total = 0;
+    for (int i = tid; i < n_items; i += kThreads) mine_all += load_item<HYB>(p, i, n_items).slabs;
+    scan(mine_all, total);
+    cut_ranges(total);
+    long long before = 0;
+    for (int i0 = 0; i0 < n_items && before < c1; i0 += kThreads) {
+      const Item it = load_item<HYB>(p, i0 + tid, n_items);
+      __syncthreads();   // the last round's sums were read
+      long long round;
+      const long long lo = before + scan(it.slabs, round);
+      place(it, i0 + tid, lo);
+      before += round;
+    }
+    __syncthreads();
+    s0 = s_start[warp];
   }
   if (!HYB) {
     // sequences of no rows give zeros
@@ -791,67 +926,15 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       if (__ldg(&p.seqlens[b]) <= 0)
         for (int i = tid; i < p.Hq * D; i += kThreads) store1(static_cast<T*>(p.out) + (size_t)b * p.Hq * D + i, 0.f);
   }
-  // ranges: per CTA, then per warp, at least kQ8MinSlabs a warp
-  const long long per_cta = max((total + gridDim.x - 1) / gridDim.x, (long long)kQ8MinSlabs * kWarps);
-  const long long c0 = min(total, per_cta * blockIdx.x), c1 = min(total, c0 + per_cta);
-  const long long per_warp = (c1 - c0 + kWarps - 1) / kWarps;
-  const long long w0 = min(c1, c0 + per_warp * warp);
-  int mine = (int)(min(c1, w0 + per_warp) - w0);
-  if (c1 > c0) {
-    long long before = 0;
-    for (int i0 = 0; i0 < n_items && before < c1; i0 += kThreads) {
-      const long long v = item_slabs<HYB>(p, i0 + tid, n_items);
-      long long incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) s_wsum[warp] = incl;
-      __syncthreads();
-      long long round = 0, off = before;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) off += s_wsum[w];
-        round += s_wsum[w];
-      }
-      const long long lo = off + incl - v, hi = off + incl;   // this item's slabs
-      if (v > 0 && hi > c0 && lo < c1) {
-        int w = lo > c0 ? (int)((lo - c0 + per_warp - 1) / per_warp) : 0;
-        for (; w < kWarps && c0 + w * per_warp < min(hi, c1); ++w) {
-          long long rel = c0 + w * per_warp - lo;
-          Start s;
-          if (HYB) {
-            int run = (i0 + tid) * 16;
-            int k = __ldcg(&p.run_slabs[run]);
-            while (rel >= k && run < (i0 + tid) * 16 + 15) {
-              rel -= k;
-              k = __ldcg(&p.run_slabs[++run]);
-            }
-            s.seg = run / p.runs_stride;
-            s.run = run - s.seg * p.runs_stride;
-            s.slab = (int)rel;
-          } else {
-            const int len = (int)(v / p.Hkv);
-            s.seg = (i0 + tid) * p.Hkv + (int)(rel / len);
-            s.run = 0;
-            s.slab = (int)(rel % len);
-          }
-          s_start[w] = s;
-        }
-      }
-      before += round;
-      __syncthreads();
-    }
-  }
-
   // ---- the warp's slabs
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::DATA;
   WarpEnd end{-1, -1, 0};
   float* scratch = p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE;
-  Warp<T, CODE, D, G, HYB> wk(p, ring, smem_u32(smem) + C::OFF_AUX + warp * C::WARP_AUX);
+  using Wk = Warp<T, CODE, D, G, HYB>;
+  Wk wk(p, ring, smem_u32(smem) + C::OFF_AUX + warp * C::WARP_AUX);
   if (mine > 0) {
-    const Start s0 = s_start[warp];
+    typename Wk::RawQ raw;
+    wk.fetch_q(s0.seg, raw);      // (arrives while the first slabs are on their way)
     wk.begin(s0);
     // does the first segment begin here?
     bool began = s0.slab == 0;
@@ -867,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       cp_async_commit();
     }
     int seg = s0.seg;
-    wk.load_q(seg);
+    wk.set_q(seg, raw);
     wk.reset();
     int si = 0, so = kStages - 1;     // the stage read next, the stage filled next
     for (int i = 0; i < mine; ++i) {
@@ -887,7 +970,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
         }
         began = true;
         seg = (int)hd.x;
-        wk.load_q(seg);
+        typename Wk::RawQ raw;
+        wk.fetch_q(seg, raw);
+        wk.set_q(seg, raw);
         wk.reset();
       }
       if (copied < mine && !wk.advance()) mine = copied;
@@ -904,7 +989,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     // is the last segment complete?  (the cursor stands on its last copied slab)
     bool last = wk.cur.at + 1 >= wk.cur.count;
     if (HYB && last) last = wk.next_run(seg, wk.cur.run + 1, wk.cur.runs) >= wk.cur.runs;
-    if (last && began) wk.write_out(seg);
+    if (p.whole) {
+      // the CTA merges the segment's states and writes it
+      end.open = seg;
+      end.began = began;
+    } else if (last && began) wk.write_out(seg);
     else if (last) {
       wk.write_state(scratch);
       end.ended = seg;
@@ -913,7 +1002,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       end.began = began;
     }
   }
-  if (lane == 0) s_end[warp] = end;
+  if (lane == 0) {
+    s_end[warp] = end;
+    s_has[warp] = end.open >= 0;
+  }
   __syncthreads();   // every ring is drained
   float* states = reinterpret_cast<float*>(smem);
   if (end.open >= 0) wk.write_state(states + warp * C::STATE);
@@ -921,7 +1013,53 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
 
   // ---- merge: chains of states of one segment across the CTA's warps
   int part_seg[2] = {-1, -1};
-  for (int col = tid; col < G * D; col += kThreads) {
+  // every warp that has a state has one of the same open segment: the maximum
+  // first, then independent terms
+  bool single = true;
+  int sseg = -1, sbegan = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const WarpEnd we = s_end[w];
+    if (we.ended >= 0) single = false;
+    if (we.open >= 0) {
+      if (sseg >= 0 && we.open != sseg) single = false;
+      sseg = we.open;
+      sbegan |= we.began;
+    }
+  }
+  if (single) {
+    if (sseg >= 0)
+      for (int col = tid; col < G * D; col += kThreads) {
+        const int h = col / D, e = col - h * D;
+        float m[kWarps], l = 0.f, a = 0.f, M = kNoRef;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          m[w] = s_has[w] ? states[w * C::STATE + h] : kNoRef;
+          M = fmaxf(M, m[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = fast_exp2(m[w] - M);
+          if (s_has[w]) {
+            l = fmaf(f, states[w * C::STATE + G + h], l);
+            a = fmaf(f, states[w * C::STATE + 2 * G + col], a);
+          }
+        }
+        if (p.whole) {
+          const int b = sseg / p.Hkv, g = sseg - b * p.Hkv;
+          store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + e, l > 0.f ? a / l : 0.f);
+        } else {
+          float* s = p.parts + ((size_t)blockIdx.x * 2 + sbegan) * C::STATE;
+          s[2 * G + col] = a;
+          if (e == 0) {
+            s[h] = M;
+            s[G + h] = l;
+          }
+        }
+      }
+    part_seg[sbegan] = sseg;
+  }
+  for (int col = tid; !single && col < G * D; col += kThreads) {
     const int h = col / D, e = col - h * D;
     Chain ch;
     ch.clear();
@@ -964,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       part_seg[cbegan ? 1 : 0] = cseg;
     }
   }
-  if (tid == 0) {
+  if (tid == 0 && !p.whole) {
     p.part_seg[2 * blockIdx.x] = part_seg[0];
     p.part_seg[2 * blockIdx.x + 1] = part_seg[1];
   }
@@ -1072,7 +1210,7 @@ cudaError_t launch_g(const Q8AttnParams& p, int grid, cudaStream_t st) {
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.run([&] { return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(kfn, dim3(grid), dim3(kThreads), C::SMEM, st, p)) != cudaSuccess) return e;
+  if ((e = launch_pdl(kfn, dim3(grid), dim3(kThreads), C::SMEM, st, p)) != cudaSuccess || p.whole) return e;
   return launch_pdl(q8_merge_kernel<T, D>, dim3(grid, G), dim3(kMergeThreads), 0, st, p);
 }
 
@@ -1103,8 +1241,12 @@ cudaError_t launch_c(const Q8AttnParams& p, int D, int grid, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms, cudaStream_t st) {
+cudaError_t launch_q8_attn(const Q8AttnParams& in, int dtype, int code, int D, int sms, cudaStream_t st) {
   const int grid = std::min(sms, kQ8MaxCtas);
+  Q8AttnParams p = in;
+  // A segment per CTA when that leaves no segment over and none is longer than
+  // kQ8WholeMax positions: one launch less than splitting.
+  p.whole = (long long)p.B * p.Hkv <= grid && p.N_max <= kQ8WholeMax;
   cudaError_t e;
   if (dtype == 0)
     e = code == kCodeE4M3 ? launch_c<__nv_bfloat16, kCodeE4M3>(p, D, grid, st)
