@@ -119,7 +119,6 @@ struct BuildBitsParams {
   uint32_t* bitmaps;         // [B, Hq, nwords]
   uint32_t* err;
   int B, Hq, N_max, nwords, k, nheads;
-  int empty_ok;              // 1: a sequence may have no rows (0: n_b counts as 1)
   uint8_t heads[128];        // the sparse heads whose sets are built
 };
 cudaError_t launch_build_bits(const BuildBitsParams& p, cudaStream_t st);

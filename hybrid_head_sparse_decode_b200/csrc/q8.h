@@ -38,7 +38,7 @@ constexpr int kQ8Warps = 16;       // warps of an attention CTA (one CTA an SM)
 constexpr int kQ8MaxCtas = 160;    // attention CTAs at most (the workspace holds that many states)
 constexpr int kQ8MinSlabs = 2;     // slabs of 16 rows a warp takes at least, while there are any
 constexpr int kQ8WholeMax = 1024;  // positions of a segment that one CTA takes alone, at most
-constexpr int kQ8Run = 256;        // positions of a run (hybrid: the unit whose rows are listed)
+constexpr int kQ8Tile = 4096;      // positions of a tile (hybrid: the unit whose rows are listed)
 struct Q8AttnParams {
   Q8Cache c;
   const void* q;             // [B, Hq, D]
@@ -52,17 +52,24 @@ struct Q8AttnParams {
   int B, Hq, Hkv, N_max;
   float scale_log2;          // log2(e) / sqrt(D)
   uint32_t role[4];          // bit h set: head h attends to every position
-  // hybrid layer only (run_slabs null: every head attends to every position)
-  uint8_t* run_slabs;        // [n_run_items * 16]: slabs of each run, [B * Hkv, runs_stride] of them
-  const uint32_t* bitmaps;   // [B, Hq, nwords]: the sparse heads' sets
+  // hybrid layer only (tile_rows null: every head attends to every position)
+  int32_t* tile_rows;        // [B * Hkv, ntiles]: rows of each tile that some head of the group uses
+  uint32_t* list_rows;       // [B * Hkv, ntiles, kQ8Tile]: in groups of sparse heads those rows (of the cache)
+  uint8_t* list_heads;       // ... and the heads of the group that use each
+  uint32_t* bitmaps;         // [B, Hq, nwords]: the sets of sparse heads beside a retrieval head
   float* logits;             // [B, Hq, N_max]: raw q.k of the retrieval heads
+  const int32_t* idx_in;     // [B, Hq, k]: sets of the sparse heads
+  int32_t* idx_out;          // [B, Hq, k]: they go on as they came
   const int32_t* k_per_seq;  // [B] or null (checked here)
-  int nwords, runs_stride, n_run_items;
+  int nwords, ntiles, k, n_sparse;
   int whole;                 // 1: CTA x takes segment x whole, nothing is left open
   // the cache's codes as rows of D bytes, boxes of sixteen rows, swizzled by D bytes
   alignas(64) CUtensorMap tmk;
   alignas(64) CUtensorMap tmv;
 };
+// The sparse heads' sets as tile_rows, list_* and bitmaps, their rows to idx_out, and
+// zeros to out (segments without rows have no other writer) (q8_sets.cu).
+cudaError_t launch_q8_sets(const Q8AttnParams& p, int dtype, int D, cudaStream_t st);
 cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms,
                            cudaStream_t st);
 

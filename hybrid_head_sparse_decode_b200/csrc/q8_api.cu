@@ -30,8 +30,9 @@ lychee_status check_q8_shape(const lychee_q8_shape* s) {
   // rows are counted in 32 bits
   if ((long long)s->num_pages * s->Hkv * s->page > 0x7fffffffLL) return LYCHEE_ERR_UNSUPPORTED;
   if ((long long)s->B * s->Hq >= (1LL << 24)) return LYCHEE_ERR_UNSUPPORTED;
-  // runs of 256 positions, over all sequences and heads, are counted in 32 bits too
-  if ((long long)s->B * s->Hkv * (((long long)s->max_pages * s->page + kQ8Run - 1) / kQ8Run) > 0x7fffffffLL)
+  // slabs of 16 rows, over all sequences and heads, are counted in 32 bits too
+  const long long n_max = (long long)s->max_pages * s->page;
+  if ((long long)s->B * s->Hkv * ((n_max + kQ8Tile - 1) / kQ8Tile) * (kQ8Tile / 16) > 0x7fffffffLL)
     return LYCHEE_ERR_UNSUPPORTED;
   return LYCHEE_OK;
 }
@@ -60,11 +61,11 @@ Q8Cache cache_of(const lychee_q8_shape* s, const lychee_q8_cache* c) {
 int n_max_of(const lychee_q8_shape* s) { return s->max_pages * s->page; }
 
 // Workspace: the states that the attention CTAs leave open; for the hybrid step
-// (k > 0) also the retrieval heads' logits, the sparse heads' bitmaps and the
-// slab counts of the runs.
+// (k > 0) also the retrieval heads' logits and the sparse heads' sets as bitmaps
+// and row lists.
 struct Q8Layout {
-  size_t part_seg, parts, scratch, logits, bitmaps, run_slabs, total;
-  int nwords, runs_stride, n_run_items;
+  size_t part_seg, parts, scratch, logits, bitmaps, tile_rows, list_rows, list_heads, total;
+  int nwords, ntiles;
 };
 Q8Layout q8_layout(const lychee_q8_shape* s, int k) {
   Q8Layout L{};
@@ -77,14 +78,18 @@ Q8Layout q8_layout(const lychee_q8_shape* s, int k) {
   if (k > 0) {
     const size_t n_max = n_max_of(s);
     L.nwords = (int)((n_max + 31) / 32);
-    L.runs_stride = (int)((n_max + kQ8Run - 1) / kQ8Run);
-    L.n_run_items = (int)(((long long)s->B * s->Hkv * L.runs_stride + 15) / 16);
+    L.ntiles = (int)((n_max + kQ8Tile - 1) / kQ8Tile);
+    const size_t tiles = (size_t)s->B * s->Hkv * L.ntiles;
     L.logits = at;
     at += align256((size_t)s->B * s->Hq * n_max * 4);
     L.bitmaps = at;
     at += align256((size_t)s->B * s->Hq * L.nwords * 4);
-    L.run_slabs = at;
-    at += align256((size_t)L.n_run_items * 16);
+    L.tile_rows = at;
+    at += align256(tiles * 4);
+    L.list_rows = at;
+    at += align256(tiles * kQ8Tile * 4);
+    L.list_heads = at;
+    at += align256(tiles * kQ8Tile);
   }
   L.total = at;
   return L;
@@ -228,31 +233,23 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   if (sms <= 0) return LYCHEE_ERR_CUDA;
   Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  uint32_t* bitmaps = reinterpret_cast<uint32_t*>(ws + L.bitmaps);
-  p.run_slabs = ws + L.run_slabs;
-  p.bitmaps = bitmaps;
+  p.tile_rows = reinterpret_cast<int32_t*>(ws + L.tile_rows);
+  p.list_rows = reinterpret_cast<uint32_t*>(ws + L.list_rows);
+  p.list_heads = ws + L.list_heads;
+  p.bitmaps = reinterpret_cast<uint32_t*>(ws + L.bitmaps);
   p.logits = reinterpret_cast<float*>(ws + L.logits);
+  p.idx_in = idx_in;
+  p.idx_out = idx_out;
   p.k_per_seq = k_per_seq;
   p.nwords = L.nwords;
-  p.runs_stride = L.runs_stride;
-  p.n_run_items = L.n_run_items;
+  p.ntiles = L.ntiles;
+  p.k = k;
+  p.n_sparse = ns;
   fill_roles(p.role, head_role, s->Hq);
   if (!encode_rows(&p.tmk, cache->k, s) || !encode_rows(&p.tmv, cache->v, s)) return LYCHEE_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (ns > 0) {
-    // the incoming sets as bitmaps; the rows go on as they came
-    BuildBitsParams bp{};
-    bp.idx_in = idx_in;
-    bp.idx_out = idx_out;
-    bp.seqlens = seqlens;
-    bp.bitmaps = bitmaps;
-    bp.err = p.err;
-    bp.B = s->B; bp.Hq = s->Hq; bp.N_max = p.N_max; bp.nwords = L.nwords; bp.k = k;
-    bp.empty_ok = 1;
-    for (int h = 0; h < s->Hq; ++h)
-      if (head_role[h] == LYCHEE_ROLE_SPARSE) bp.heads[bp.nheads++] = (uint8_t)h;
-    if (timed(kKindBuildBits, cs, [&] { return launch_build_bits(bp, cs); }) != cudaSuccess) return LYCHEE_ERR_CUDA;
-  }
+  if (timed(kKindBuildBits, cs, [&] { return launch_q8_sets(p, s->dtype, s->d, cs); }) != cudaSuccess)
+    return LYCHEE_ERR_CUDA;
   if (timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); }) != cudaSuccess)
     return LYCHEE_ERR_CUDA;
   if (ns == s->Hq) return LYCHEE_OK;

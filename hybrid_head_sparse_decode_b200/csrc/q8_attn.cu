@@ -62,12 +62,16 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
 constexpr float kRefSlack = 15.f;    // and moves when a weight passes it by more than this
+constexpr uint32_t kAbsent = 0xffffffffu;  // of a slab's rows: none
 constexpr float kNoRef = -1e30f;     // no row yet (finite: differences of two stay numbers)
 constexpr uint32_t kFullSlab = 1u << 29;   // stage header: sixteen rows of one page, one scale
 constexpr uint32_t kAllHeads = 1u << 30;   // ... and every head uses every row
 
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -91,6 +95,12 @@ __device__ __forceinline__ uint32_t lds_u(uint32_t a) {
 }
 __device__ __forceinline__ void sts_u(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -157,6 +167,13 @@ __device__ __forceinline__ float4 load_q4<float>(const float* p) {
 }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
 
 template <typename T, int CODE, int D, int G>
 struct Cfg {
@@ -170,10 +187,10 @@ struct Cfg {
   static constexpr int VB = D / 8;                       // bytes of V a lane takes of each of its four rows
   static constexpr int DATA = 32 * D;                    // a stage's rows: K, then V
   static constexpr int OFF_V = 16 * D;
-  // beside the rows, per stage: row scales (K; log2 of V's), positions and heads, header
-  static constexpr int AUX_S = 0, AUX_META = 128, AUX_HEAD = 192, AUX = 208;
-  static constexpr int LIST = kQ8Run * 2;                // a run's rows (hybrid): u16 each
-  static constexpr int WARP_AUX = kStages * AUX + LIST + 32;   // and the stages' mbarriers
+  // beside the rows, per stage: row scales (K's, V's), the rows each head uses
+  // (u16 a head), the header {segment, position | flags, K scale, V scale}
+  static constexpr int AUX_S = 0, AUX_META = 128, AUX_HEAD = 144, AUX = 160;
+  static constexpr int WARP_AUX = kStages * AUX + 32;    // and the stages' mbarriers
   static constexpr int OFF_AUX = kWarps * kStages * DATA;
   static constexpr int STATE = G * (D + 2);              // floats of a state: m[G], l[G], acc[G][D]
   static constexpr int SMEM = OFF_AUX + kWarps * WARP_AUX + 1024;   // + alignment slack
@@ -184,38 +201,33 @@ struct Cfg {
 
 // Where a range of slabs begins.
 struct Start {
-  int seg, run, slab;   // segment b * Hkv + g; hybrid: run of the segment, slab of the run
-};
-
-// A warp's place in its slabs: the next one to copy.
-struct Cursor {
-  int seg, b, g, n;
-  int at, count;        // dense: slab of the segment, slabs of it.  hybrid: slab of the run, slabs of it
-  int run, runs;        // hybrid
-  int rows;             // hybrid: rows of the run
-  bool packed;          // hybrid: the run's rows are consecutive
-  int win;              // dense: the slab that lane 0's table entry belongs to
-  int page;             // this lane's table entry of the window / run (-1: not a page)
-  float ks, lv;         // ... and the block's scales: K's, log2 of V's
+  int seg, tile, slab;  // segment b * Hkv + g; hybrid: tile of the segment, slab of the tile
 };
 
 template <typename T, int CODE, int D, int G, bool HYB>
 struct Warp {
   using C = Cfg<T, CODE, D, G>;
   const Q8AttnParams& p;
-  uint32_t ring, aux, list, bars;
+  uint32_t ring, aux, bars;
   int lane, r, c;
-  Cursor cur;
-  uint32_t parity;      // bit i: the phase that stage i's mbarrier completes next
   uint32_t gathered;    // bit i: stage i was last filled row by row
-  bool mixed;           // hybrid: the cursor's group has a sparse head
+
+  // The warp's place in its slabs: the next one to copy.
+  int seg, b, g, n;
+  int at, rows;         // slab of the segment (hybrid: of the tile), rows of it
+  int tile;             // hybrid (else 0)
+  bool sparse, mixed;   // hybrid: the group has sparse heads only / has some
+  // ... and what was loaded for it: the page (consecutive rows) or this lane's row
+  uint32_t pre, pre_m;  // hybrid: the rows that head `lane` uses, or the heads that use this lane's row
 
   __device__ __forceinline__ Warp(const Q8AttnParams& pp, uint32_t ring_, uint32_t aux_)
-      : p(pp), ring(ring_), aux(aux_), list(aux_ + kStages * C::AUX), bars(aux_ + kStages * C::AUX + C::LIST) {
+      : p(pp), ring(ring_), aux(aux_), bars(aux_ + kStages * C::AUX) {
     lane = threadIdx.x & 31;
     r = lane >> 2;
     c = lane & 3;
-    parity = gathered = 0;
+    gathered = 0;
+    tile = 0;
+    sparse = mixed = false;
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < kStages; ++i)
@@ -224,222 +236,173 @@ struct Warp {
     }
     __syncwarp();
   }
-  __device__ __forceinline__ int length(int b) const { return min(max(__ldg(&p.seqlens[b]), 0), p.N_max); }
-
   __device__ __forceinline__ bool retrieval(int h) const { return (p.role[h >> 5] >> (h & 31)) & 1u; }
-  // This lane's table entry at position `pos` (want: there is one), and its scales.
-  __device__ __forceinline__ void load_page(bool want, int pos) {
-    cur.page = want ? __ldg(&p.c.table[(size_t)cur.b * p.c.max_pages + (pos >> p.c.page_log2)]) : -1;
-    const bool ok = cur.page >= 0 && cur.page < p.c.num_pages;
-    if (want && !ok) flag_error(p.err, kErrBadIndex);
-    if (!ok) cur.page = -1;
-    const int unit = max(cur.page, 0) * p.Hkv + cur.g;
-    cur.ks = __ldg(&p.c.k_scale[unit]);
-    cur.lv = fast_log2(__ldg(&p.c.v_scale[unit]));
-  }
 
   // ---- the cursor
-  __device__ __forceinline__ void enter(int seg) {
-    cur.seg = seg;
-    cur.b = seg / p.Hkv;
-    cur.g = seg - cur.b * p.Hkv;
-    cur.n = length(cur.b);
-    cur.at = 0;
-    cur.win = -64;
+  __device__ __forceinline__ void enter(int seg_) {
+    seg = seg_;
+    b = seg / p.Hkv;
+    g = seg - b * p.Hkv;
+    n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
+    at = 0;
     if (HYB) {
-      cur.run = 0;
-      cur.runs = (cur.n + kQ8Run - 1) / kQ8Run;
-      mixed = false;
+      int kept = 0;
 #pragma unroll
-      for (int t = 0; t < G; ++t) mixed = mixed || !retrieval(cur.g * G + t);
+      for (int t = 0; t < G; ++t) kept += retrieval(g * G + t);
+      sparse = kept == 0;
+      mixed = kept > 0 && kept < G;
     } else {
-      cur.count = (cur.n + 15) >> 4;
+      rows = n;
     }
   }
-  // The first run at or after `from` that holds a row (`upto` if none does).
-  __device__ __forceinline__ int next_run(int seg, int from, int upto) const {
-    const uint8_t* s = p.run_slabs + (size_t)seg * p.runs_stride;
-    for (int i0 = from; i0 < upto; i0 += 128) {
-      uint32_t k[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 32 * j + lane;
-        k[j] = i < upto ? __ldcg(s + i) : 0u;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t m = __ballot_sync(kFull, k[j] != 0);
-        if (m) return i0 + 32 * j + __ffs(m) - 1;
-      }
-    }
-    return upto;
-  }
-  // To the first segment after cur.seg that has positions; false if there is none.
+  // To the first segment after `seg` that has positions; false if there is none.
   __device__ __forceinline__ bool enter_next() {
-    int seg = cur.seg + 1;
-    while (seg < p.B * p.Hkv) {
-      enter(seg);
-      if (cur.n > 0) return true;
-      seg = (cur.b + 1) * p.Hkv;
+    int s = seg + 1;
+    while (s < p.B * p.Hkv) {
+      enter(s);
+      if (n > 0) return true;
+      s = (b + 1) * p.Hkv;
     }
     return false;
   }
-  // The rows of run cur.run into the list: entry = position in the run | heads << 8.
-  __device__ __forceinline__ void build_run() {
-    const int base = cur.run * kQ8Run;
-    const int word = lane >> 2, shift = (lane & 3) * 8;   // eight positions a lane
-    const int pos0 = base + lane * 8;
-    const int left = min(max(cur.n - pos0, 0), 8);
-    const uint32_t in = (1u << left) - 1u;
-    load_page(lane < (kQ8Run >> p.c.page_log2) && base + (lane << p.c.page_log2) < cur.n,
-              base + (lane << p.c.page_log2));
-    uint32_t bits[G], u = 0;
-#pragma unroll
-    for (int t = 0; t < G; ++t) {
-      const int h = cur.g * G + t;
-      if (retrieval(h)) bits[t] = in;
-      else {
-        const int w = (base >> 5) + word;
-        const uint32_t x = w < p.nwords
-                               ? __ldcg(&p.bitmaps[((size_t)cur.b * p.Hq + h) * p.nwords + w]) : 0u;
-        bits[t] = (x >> shift) & in;
-      }
-      u |= bits[t];
-    }
-    const int mine = __popc(u);
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += y;
-    }
-    cur.rows = __shfl_sync(kFull, incl, 31);
-    cur.count = (cur.rows + 15) >> 4;
-    cur.packed = cur.rows == min(cur.n - base, kQ8Run);
-    int slot = incl - mine;
-    __syncwarp();   // the previous run's entries were read
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((u >> i) & 1u) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int t = 0; t < G; ++t) m |= ((bits[t] >> i) & 1u) << t;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(list + 2 * slot), "h"((uint16_t)((lane * 8 + i) | (m << 8))) : "memory");
-        ++slot;
+  // Hybrid: to the first tile of the segment at or after `from` that has rows; false
+  // if none does.
+  __device__ __forceinline__ bool enter_tile(int from) {
+    for (int t0 = from; t0 * kQ8Tile < n; t0 += 32) {
+      const int k = (t0 + lane) * kQ8Tile < n ? __ldcg(&p.tile_rows[(size_t)seg * p.ntiles + t0 + lane]) : 0;
+      const uint32_t any = __ballot_sync(kFull, k > 0);
+      if (any) {
+        const int l = __ffs(any) - 1;
+        tile = t0 + l;
+        rows = __shfl_sync(kFull, k, l);
+        at = 0;
+        return true;
       }
     }
-    __syncwarp();
+    return false;
   }
-  __device__ __forceinline__ void begin(const Start& s) {
+  // Start loading what the slab at the cursor needs.
+  __device__ __forceinline__ void preload() {
+    if (HYB && sparse) {
+      const int e = 16 * at + (lane & 15);
+      const size_t from = ((size_t)seg * p.ntiles + tile) * kQ8Tile + e;
+      pre = kAbsent;
+      pre_m = 0;
+      if (e < rows) {
+        pre = __ldcg(p.list_rows + from);
+        pre_m = __ldcg(p.list_heads + from);
+      }
+    } else {
+      const int pos0 = tile * kQ8Tile + 16 * at;
+      pre = __ldg(&p.c.table[(size_t)b * p.c.max_pages + (pos0 >> p.c.page_log2)]);
+      if (HYB && mixed) {
+        pre_m = 0xffffu;
+        if (lane < G && !retrieval(g * G + lane))
+          pre_m = __ldcg(reinterpret_cast<const uint16_t*>(p.bitmaps) +
+                         ((size_t)b * p.Hq + g * G + lane) * p.nwords * 2 + (pos0 >> 4));
+      }
+    }
+  }
+  __device__ __forceinline__ bool begin(const Start& s) {
+    if (s.seg >= p.B * p.Hkv) return false;
     enter(s.seg);
-    if (HYB) {
-      cur.run = s.run;
-      build_run();
-    }
-    cur.at = s.slab;
+    if (HYB && !enter_tile(s.tile)) return false;
+    at = s.slab;
+    preload();
+    return true;
   }
-  // To the next slab.  false: there is none (never, unless lengths or sets change
-  // under the call).
+  // To the next slab; false: there is none.
   __device__ __forceinline__ bool advance() {
-    if (++cur.at < cur.count) return true;
-    if (HYB) {
-      int run = next_run(cur.seg, cur.run + 1, cur.runs);
-      while (run >= cur.runs) {
-        if (!enter_next()) return false;
-        run = next_run(cur.seg, 0, cur.runs);
+    if (16 * ++at >= rows) {
+      if (HYB) {
+        if (!enter_tile(tile + 1)) {
+          do {
+            if (!enter_next()) return false;
+          } while (!enter_tile(0));
+        }
+      } else if (!enter_next()) {
+        return false;
       }
-      cur.run = run;
-      cur.at = 0;
-      build_run();
-      return true;
     }
-    return enter_next();
+    preload();
+    return true;
+  }
+  // Hybrid: no tile before `t` has rows.
+  __device__ __forceinline__ bool first_tile(int seg_, int t) const {
+    for (int t0 = 0; t0 < t; t0 += 32)
+      if (__any_sync(kFull, t0 + lane < t && __ldcg(&p.tile_rows[(size_t)seg_ * p.ntiles + t0 + lane]) > 0)) return false;
+    return true;
   }
 
   // ---- the slab at the cursor into stage `si`
   __device__ __forceinline__ void copy(int si) {
-    const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX;
-    const int log2p = p.c.page_log2, pmask = (1 << log2p) - 1;
+    const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX, bar = bars + 8 * si;
+    const int log2p = p.c.page_log2;
     const int i = lane & 15;
-    int e_at = 16 * cur.at + i;           // hybrid: this lane's row of the run
-    uint32_t myrow = 0, meta;
-    bool in;
-    float ks, lv;
-    if (!HYB || cur.packed) {
+    uint32_t myrow, heads, flags = 0;     // this lane's row; lane t: the rows head t uses
+    if (!HYB || !sparse) {
       // consecutive positions, all in one page (pages are whole slabs)
-      int pos0, wl;
-      if (HYB) {
-        pos0 = cur.run * kQ8Run + 16 * cur.at;
-        wl = (16 * cur.at) >> log2p;
-      } else {
-        pos0 = 16 * cur.at;
-        if ((unsigned)(cur.at - cur.win) >= 32u) {
-          cur.win = cur.at;
-          load_page(cur.at + lane < cur.count, 16 * (cur.at + lane));
+      const int pos0 = tile * kQ8Tile + 16 * at;
+      const bool ok = pre < (uint32_t)p.c.num_pages;
+      if (!ok && lane == 0) flag_error(p.err, kErrBadIndex);
+      const int unit = (int)pre * p.Hkv + g;
+      const uint32_t row0 = ((uint32_t)unit << log2p) + (pos0 & ((1 << log2p) - 1));
+      const int left = ok ? n - pos0 : 0;
+      flags = (uint32_t)pos0;
+      if (left >= 16) {
+        if (lane == 0) {
+          if ((gathered >> si) & 1u) fence_proxy_async_smem();   // ordinary writes before the TMA's
+          sts64(ax + C::AUX_HEAD, (uint32_t)seg, flags | kFullSlab | (HYB && mixed ? 0u : kAllHeads));
+          copy4(ax + C::AUX_HEAD + 8, p.c.k_scale + unit);       // the block's two scales
+          copy4(ax + C::AUX_HEAD + 12, p.c.v_scale + unit);
+          asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+          asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((uint32_t)C::DATA)
+                       : "memory");
+          const uint64_t policy = l2_evict_first_policy();
+          tma_rows(st, &p.tmk, (int)row0, bar, policy);
+          tma_rows(st + C::OFF_V, &p.tmv, (int)row0, bar, policy);
         }
-        wl = cur.at - cur.win;
-      }
-      const int page = __shfl_sync(kFull, cur.page, wl);
-      const uint32_t row0 = ((uint32_t)(page * p.Hkv + cur.g) << log2p) + (pos0 & pmask);
-      const bool full = page >= 0 && cur.n - pos0 >= 16;
-      if (full && lane == 0) {
-        const uint32_t bar = bars + 8 * si;
-        if ((gathered >> si) & 1u) fence_proxy_async_smem();   // ordinary writes before the TMA's
-        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((uint32_t)C::DATA)
-                     : "memory");
-        const uint64_t policy = l2_evict_first_policy();
-        tma_rows(st, &p.tmk, (int)row0, bar, policy);
-        tma_rows(st + C::OFF_V, &p.tmv, (int)row0, bar, policy);
-      }
-      ks = __shfl_sync(kFull, cur.ks, wl);
-      lv = __shfl_sync(kFull, cur.lv, wl);
-      uint32_t heads = 0xffu;
-      if (HYB && mixed && e_at < cur.rows) {
-        uint16_t e;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * e_at));
-        heads = e >> 8;
-      }
-      if (full) {
-        if (HYB && mixed && lane < 16) sts_u(ax + C::AUX_META + lane * 4, heads << 24);
-        if (lane == 0)
-          sts128(ax + C::AUX_HEAD, (uint32_t)cur.seg, (uint32_t)pos0 | kFullSlab | (HYB && mixed ? 0u : kAllHeads),
-                 __float_as_uint(ks), __float_as_uint(lv));
+        if (HYB && mixed && lane < G) sts16(ax + C::AUX_META + 2 * lane, pre_m);
         gathered &= ~(1u << si);
         return;
       }
-      in = page >= 0 && i < cur.n - pos0;
-      myrow = row0 + i;
-      meta = in ? heads << 24 : 0u;
-      if (HYB) meta |= (uint32_t)(pos0 + i);
+      myrow = i < left ? row0 + i : kAbsent;
+      heads = ((1u << max(left, 0)) - 1u) & (HYB && mixed ? pre_m : 0xffffu);
     } else {
-      uint16_t e = 0;
-      if (e_at < cur.rows) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(list + 2 * e_at));
-      const int off = e & 255, wl = off >> log2p;
-      const int page = __shfl_sync(kFull, cur.page, wl);
-      ks = __shfl_sync(kFull, cur.ks, wl);
-      lv = __shfl_sync(kFull, cur.lv, wl);
-      in = e_at < cur.rows && page >= 0;
-      myrow = ((uint32_t)(page * p.Hkv + cur.g) << log2p) + (off & pmask);   // (a run begins on a page)
-      meta = in ? (uint32_t)(e >> 8) << 24 : 0u;
+      myrow = pre;
+      heads = 0;
+#pragma unroll
+      for (int t = 0; t < G; ++t) {
+        const uint32_t m = __ballot_sync(kFull, lane < 16 && ((pre_m >> t) & 1u));
+        if (lane == t) heads = m;
+      }
     }
-    // row by row; lane i (and i + 16) knows row i.  An absent row is zeros with scale 1.
+    // row by row; lane i (and i + 16) knows row i.  Absent rows are zeros with scale 1.
     gathered |= 1u << si;
-    if (!in) myrow = 0xffffffffu;
     constexpr int LPR = D / 16, RPI = 32 / LPR;   // lanes a row, rows an instruction
     const int lr = lane / LPR, q = lane % LPR;
 #pragma unroll
     for (int j = 0; j < 16 / RPI; ++j) {
       const int R = RPI * j + lr;
       const uint32_t row = __shfl_sync(kFull, myrow, R);
-      const bool have = row != 0xffffffffu;
-      const size_t at = have ? (size_t)row * D + 16 * q : 0;
       const uint32_t dst = st + R * D + ((D == 128 ? q ^ (R & 7) : q ^ ((R >> 1) & 3)) << 4);
-      cp_async16z(dst, p.c.k + at, have ? 16u : 0u);
-      cp_async16z(dst + C::OFF_V, p.c.v + at, have ? 16u : 0u);
+      const uint32_t from = 16 * q;
+      if (row != kAbsent) {
+        copy16(dst, p.c.k + ((size_t)row * D + from));
+        copy16(dst + C::OFF_V, p.c.v + ((size_t)row * D + from));
+      } else {
+        sts128(dst, 0u, 0u, 0u, 0u);
+        sts128(dst + C::OFF_V, 0u, 0u, 0u, 0u);
+      }
     }
-    sts_u(ax + C::AUX_S + lane * 4, __float_as_uint(!in ? (lane < 16 ? 1.f : 0.f) : lane < 16 ? ks : lv));
-    if (lane < 16) sts_u(ax + C::AUX_META + lane * 4, meta);
-    if (lane == 0) sts128(ax + C::AUX_HEAD, (uint32_t)cur.seg, 0u, 0u, 0u);
+    if (myrow != kAbsent) copy4(ax + C::AUX_S + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + (myrow >> log2p));
+    else sts_u(ax + C::AUX_S + lane * 4, __float_as_uint(1.f));
+    if (lane < G) sts16(ax + C::AUX_META + 2 * lane, heads);
+    if (lane == 0) sts64(ax + C::AUX_HEAD, (uint32_t)seg, flags);
+    // the phase ends when every lane's copies have landed
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
   }
 
   // ---- the heads' states
@@ -452,29 +415,30 @@ struct Warp {
 
   size_t logit_row;               // hybrid: where this lane's first column's logits go
   int logit_cols;                 // ... bit j: column j is a retrieval head (written by this lane)
+  bool retrieves;                 // ... the group has a retrieval head
 
   struct RawQ {
     float4 x[C::KM];
   };
-  __device__ __forceinline__ void fetch_q(int seg, RawQ& raw) const {
-    const int b = seg / p.Hkv, g = seg - b * p.Hkv;
+  __device__ __forceinline__ void fetch_q(int sg, RawQ& raw) const {
     const int t = C::kBeside ? r & 3 : r;
 #pragma unroll
     for (int m = 0; m < C::KM; ++m) {
       raw.x[m] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < G)
-        raw.x[m] = load_q4<T>(static_cast<const T*>(p.q) + ((size_t)b * p.Hq + g * G + t) * D + (m >> 2) * 64 +
+        raw.x[m] = load_q4<T>(static_cast<const T*>(p.q) + ((size_t)sg * G + t) * D + (m >> 2) * 64 +
                               16 * c + 4 * (m & 3));
     }
   }
-  __device__ __forceinline__ void set_q(int seg, const RawQ& q) {
+  __device__ __forceinline__ void set_q(int sg, const RawQ& q) {
     if (HYB) {
-      const int b = seg / p.Hkv, g = seg - b * p.Hkv;
-      logit_row = ((size_t)b * p.Hq + g * G + column_head(0)) * p.N_max;
+      const int h0 = sg % p.Hkv * G;
+      logit_row = ((size_t)sg * G + column_head(0)) * p.N_max;
       logit_cols = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        if (column_head(j) < G && (!C::kBeside || c < 2) && retrieval(g * G + column_head(j))) logit_cols |= 1 << j;
+        if (column_head(j) < G && (!C::kBeside || c < 2) && retrieval(h0 + column_head(j))) logit_cols |= 1 << j;
+      retrieves = __any_sync(kFull, logit_cols != 0);
     }
     const float4 (&x)[C::KM] = q.x;
     float mx = 0.f;
@@ -530,7 +494,7 @@ struct Warp {
   }
 
   // ---- one slab: stage `si`, its header in hd
-  __device__ __forceinline__ void consume(int si, uint4 hd, int seg) {
+  __device__ __forceinline__ void consume(int si, uint4 hd) {
     const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX;
     const int R = r ^ ((r & 1) << 2);      // this lane's rows of S: R and R + 8
     // ---- S
@@ -566,20 +530,21 @@ struct Warp {
       for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(kFull, s[i], 2);
     }
     // s[0], s[1]: row R, columns 2c and 2c + 1; s[2], s[3]: row R + 8
-    const bool full = hd.y & kFullSlab;
-    float sk[2] = {__uint_as_float(hd.z), __uint_as_float(hd.z)}, lv[2] = {__uint_as_float(hd.w), __uint_as_float(hd.w)};
-    uint32_t meta[2] = {0xff000000u, 0xff000000u};
-    if (!full) {
+    float sk[2], sv[2];
+    sk[0] = sk[1] = __uint_as_float(hd.z);
+    sv[0] = sv[1] = __uint_as_float(hd.w);
+    if (!(hd.y & kFullSlab)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sk[i] = lds_f(ax + C::AUX_S + (R + 8 * i) * 4);
-        lv[i] = lds_f(ax + C::AUX_S + (16 + R + 8 * i) * 4);
-        meta[i] = lds_u(ax + C::AUX_META + (R + 8 * i) * 4);
+        sv[i] = lds_f(ax + C::AUX_S + (16 + R + 8 * i) * 4);
       }
-    } else if (HYB && !(hd.y & kAllHeads)) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) meta[i] = lds_u(ax + C::AUX_META + (R + 8 * i) * 4);
     }
+    const float lv[2] = {fast_log2(sv[0]), fast_log2(sv[1])};
+    const float inv[2] = {fast_exp2(-lv[0]), fast_exp2(-lv[1])};
+    // bit 16 j + R + 8 i: row R + 8 i counts for column j's head
+    uint32_t used = 0xffffffffu;
+    if (!(hd.y & kAllHeads)) used = lds_u(ax + C::AUX_META + 2 * column_head(0)) >> R;
     // t: log2 of a row's weight times its scale, -inf where a head does not use it.
     // (Columns beyond the group's heads hold zero queries; nothing reads them.)
     float t[4];
@@ -588,20 +553,20 @@ struct Warp {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float raw = s[2 * i + j] * (sk[i] * fq[j]);
-        const int h = column_head(j);
-        if (HYB) {
-          const bool on = (meta[i] >> (24 + (h & 7))) & 1u;
-          if (on && ((logit_cols >> j) & 1)) {
-            const int pos = full ? (int)(hd.y & 0xffffffu) + R + 8 * i : (int)(meta[i] & 0xffffffu);
-            p.logits[logit_row + (size_t)j * p.N_max + pos] = raw;
-          }
-          t[2 * i + j] = on ? fmaf(raw, p.scale_log2, lv[i]) : -INFINITY;
-        } else {
-          t[2 * i + j] = meta[i] ? fmaf(raw, p.scale_log2, lv[i]) : -INFINITY;
-        }
+        s[2 * i + j] *= sk[i] * fq[j];
+        const bool on = (used >> (16 * j + 8 * i)) & 1u;
+        t[2 * i + j] = on ? fmaf(s[2 * i + j], p.scale_log2, lv[i]) : -INFINITY;
         over = over || t[2 * i + j] > ref[j] + kRefSlack;
       }
+    if (HYB && retrieves) {
+      // (a group with a retrieval head has consecutive rows)
+      float* out = p.logits + logit_row + ((hd.y & 0xffffffu) + R);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (((logit_cols >> j) & 1) && ((used >> (16 * j + 8 * i)) & 1u)) out[(size_t)j * p.N_max + 8 * i] = s[2 * i + j];
+    }
     if (__any_sync(kFull, over)) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -626,11 +591,10 @@ struct Warp {
     float w[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float inv = fast_exp2(-lv[i]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         w[2 * i + j] = fast_exp2(t[2 * i + j] - ref[j]);
-        l[j] = fmaf(w[2 * i + j], inv, l[j]);
+        l[j] = fmaf(w[2 * i + j], inv[i], l[j]);
       }
     }
     uint32_t pb[C::kTwo && !C::kBeside ? 2 : 1][2];
@@ -688,15 +652,14 @@ struct Warp {
     }
   }
   // Dimension of acc[m][2 * i + j]: chunk r, byte 2 m + i of it.
-  __device__ __forceinline__ void write_out(int seg) {
+  __device__ __forceinline__ void write_out(int sg) {
     finish();
-    const int b = seg / p.Hkv, g = seg - b * p.Hkv;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int h = column_head(j);
       if (h >= G || (C::kBeside && c >= 2)) continue;
       const float inv = l[j] > 0.f ? 1.f / l[j] : 0.f;
-      T* o = static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + r * C::VB;
+      T* o = static_cast<T*>(p.out) + ((size_t)sg * G + h) * D + r * C::VB;
 #pragma unroll
       for (int m = 0; m < C::KM; ++m) {
         store1(o + 2 * m, acc[m][j] * inv);
@@ -714,12 +677,9 @@ struct Warp {
         s[h] = ref[j];
         s[G + h] = l[j];
       }
-      float* o = s + 2 * G + h * D + r * C::VB;
+      float2* o = reinterpret_cast<float2*>(s + 2 * G + h * D + r * C::VB);
 #pragma unroll
-      for (int m = 0; m < C::KM; ++m) {
-        o[2 * m] = acc[m][j];
-        o[2 * m + 1] = acc[m][2 + j];
-      }
+      for (int m = 0; m < C::KM; ++m) o[m] = make_float2(acc[m][j], acc[m][2 + j]);
     }
   }
 };
@@ -744,74 +704,38 @@ struct Chain {
   }
 };
 
-__device__ __forceinline__ int warp_sum_int(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
+// What the ranges are counted in: sequences (dense: the slabs of all their KV
+// heads), or the tiles of the segments (hybrid).  (The host keeps all slabs of a
+// call below 2^31.)
+template <bool HYB>
+__device__ __forceinline__ int item_slabs(const Q8AttnParams& p, int i, int n_items) {
+  if (i >= n_items) return 0;
+  if (HYB) return (__ldcg(&p.tile_rows[i]) + 15) >> 4;
+  return ((min(max(__ldg(&p.seqlens[i]), 0), p.N_max) + 15) >> 4) * p.Hkv;
+}
+// Slab `rel` of item i, which has `slabs`.
+template <bool HYB>
+__device__ __forceinline__ Start start_at(const Q8AttnParams& p, int slabs, int i, int rel) {
+  if (HYB) {
+    const int seg = i / p.ntiles;
+    return Start{seg, i - seg * p.ntiles, rel};
+  }
+  const int len = slabs / p.Hkv, g = rel / len;
+  return Start{i * p.Hkv + g, 0, rel - g * len};
 }
 
-// What the ranges are counted in: sequences (dense: the slabs of all their KV
-// heads), or sixteen runs (hybrid).
-struct Item {
-  uint4 runs;           // hybrid: the slab counts, a byte each
-  long long slabs;
-};
-template <bool HYB>
-__device__ __forceinline__ Item load_item(const Q8AttnParams& p, int i, int n_items) {
-  Item it{make_uint4(0u, 0u, 0u, 0u), 0};
-  if (i >= n_items) return it;
-  if (HYB) {
-    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(p.run_slabs) + i);
-    it.runs = x;
-    it.slabs = (long long)__dp4a(
-        x.x, 0x01010101u, __dp4a(x.y, 0x01010101u, __dp4a(x.z, 0x01010101u, __dp4a(x.w, 0x01010101u, 0u))));
-  } else {
-    const int n = min(max(__ldg(&p.seqlens[i]), 0), p.N_max);
-    it.slabs = (long long)((n + 15) >> 4) * p.Hkv;
-  }
-  return it;
-}
-// Slab `rel` of item i.
-template <bool HYB>
-__device__ __forceinline__ Start start_at(const Q8AttnParams& p, const Item& it, int i, int rel) {
-  Start s;
-  if (HYB) {
-    const uint32_t w[4] = {it.runs.x, it.runs.y, it.runs.z, it.runs.w};
-    int at = 0;
-    bool found = false;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int k = (int)((w[j >> 2] >> (8 * (j & 3))) & 255u);
-      if (!found) {
-        if (rel < k) found = true;
-        else {
-          rel -= k;
-          at = min(at + 1, 15);
-        }
-      }
-    }
-    const int run = i * 16 + at;
-    s.seg = run / p.runs_stride;
-    s.run = run - s.seg * p.runs_stride;
-    s.slab = rel;
-  } else {
-    const int len = (int)it.slabs / p.Hkv;
-    s.seg = i * p.Hkv + rel / len;
-    s.run = 0;
-    s.slab = rel % len;
-  }
-  return s;
-}
+constexpr int kEntries = 2 * kWarps;   // states in a CTA's merge: each warp's ended one, then its open one
 
 template <typename T, int CODE, int D, int G, bool HYB>
 __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_constant__ Q8AttnParams p) {
   using C = Cfg<T, CODE, D, G>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ long long s_wsum[kWarps];
-  __shared__ Start s_start[kWarps];
+  __shared__ int s_wsum[kWarps];
+  __shared__ int3 s_at[kWarps];
   __shared__ WarpEnd s_end[kWarps];
-  __shared__ int s_has[kWarps];
+  __shared__ float s_f[G][32], s_l[G][32], s_m[G][32];
+  __shared__ uint32_t s_first, s_valid;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   if (tid == 0) {
@@ -827,39 +751,42 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       if (n < 0 || n > p.N_max) flag_error(p.err, kErrBadSeqlen);
       if (HYB && p.k_per_seq && n > 0 && __ldg(&p.k_per_seq[b]) < 1) flag_error(p.err, kErrBadBudget);
     }
-  const int n_items = HYB ? p.n_run_items : p.B;
+  const int n_items = HYB ? p.B * p.Hkv * p.ntiles : p.B;
   Start s0{0, 0, 0};
   int mine = 0;
   // the ranges of [0, total): per CTA, at least kQ8MinSlabs a warp, then per warp
-  long long c0 = 0, c1 = 0, per_warp = 1;
-  auto cut_ranges = [&](long long total) {
-    const long long per_cta = max((total + gridDim.x - 1) / gridDim.x, (long long)kQ8MinSlabs * kWarps);
-    c0 = min(total, per_cta * blockIdx.x);
-    c1 = min(total, c0 + per_cta);
-    per_warp = max((c1 - c0 + kWarps - 1) / kWarps, 1LL);
-    const long long w0 = min(c1, c0 + per_warp * warp);
-    mine = (int)(min(c1, w0 + per_warp) - w0);
+  int c0 = 0, c1 = 0, per_warp = 1;
+  auto cut_ranges = [&](int total) {
+    const int per_cta = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kQ8MinSlabs * kWarps);
+    c0 = (int)min((long long)total, (long long)per_cta * blockIdx.x);
+    c1 = (int)min((long long)total, (long long)c0 + per_cta);
+    per_warp = max((c1 - c0 + kWarps - 1) / kWarps, 1);
+    const int w0 = min(c1, c0 + per_warp * warp);
+    mine = min(c1 - w0, per_warp);
   };
-  // the warps whose ranges begin in [lo, lo + it.slabs)
-  auto place = [&](const Item& it, int i, long long lo) {
-    const long long hi = lo + it.slabs;
-    if (it.slabs > 0 && hi > c0 && lo < c1) {
-      int w = lo > c0 ? (int)((lo - c0 + per_warp - 1) / per_warp) : 0;
-      for (; w < kWarps && c0 + w * per_warp < min(hi, c1); ++w)
-        s_start[w] = start_at<HYB>(p, it, i, (int)(c0 + w * per_warp - lo));
+  // hands the item to the warps whose ranges begin in [lo, lo + slabs)
+  auto place = [&](int slabs, int i, int lo) {
+    const int hi = lo + slabs;
+    if (slabs > 0 && hi > c0 && lo < c1) {
+      int w = lo > c0 ? (lo - c0 + per_warp - 1) / per_warp : 0;
+      for (; w < kWarps && c0 + w * per_warp < min(hi, c1); ++w) s_at[w] = make_int3(i, lo, slabs);
     }
   };
+  auto my_start = [&]() {
+    __syncthreads();
+    if (mine > 0) s0 = start_at<HYB>(p, s_at[warp].z, s_at[warp].x, c0 + warp * per_warp - s_at[warp].y);
+  };
   // exclusive prefix of v over the CTA's threads; `sum` gets the total
-  auto scan = [&](long long v, long long& sum) {
-    long long incl = v;
+  auto scan = [&](int v, int& sum) {
+    int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(kFull, incl, o);
+      const int y = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += y;
     }
     if (lane == 31) s_wsum[warp] = incl;
     __syncthreads();
-    long long off = 0;
+    int off = 0;
     sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -871,54 +798,35 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   if (p.whole) {
     // segment blockIdx.x is this CTA's
     if ((int)blockIdx.x < p.B * p.Hkv) {
-      int k = 0, runs = 0;   // hybrid: this lane's run (there are at most 32), the runs before it
-      int total;
-      if (HYB) {
-        if (lane < p.runs_stride) k = __ldcg(&p.run_slabs[(size_t)blockIdx.x * p.runs_stride + lane]);
-        runs = k;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kFull, runs, o);
-          if (lane >= o) runs += y;
-        }
-        total = __shfl_sync(kFull, runs, 31);
-      } else {
-        total = (min(max(__ldg(&p.seqlens[blockIdx.x / p.Hkv]), 0), p.N_max) + 15) >> 4;
-      }
-      const int per = (total + kWarps - 1) / kWarps, w0 = min(total, per * warp);
+      // (hybrid: it has one tile, its rows below kQ8WholeMax)
+      const int rows = HYB ? __ldcg(&p.tile_rows[blockIdx.x]) : min(max(__ldg(&p.seqlens[blockIdx.x / p.Hkv]), 0), p.N_max);
+      const int total = (rows + 15) >> 4, per = (total + kWarps - 1) / kWarps, w0 = min(total, per * warp);
       mine = min(total, w0 + per) - w0;
       s0.seg = blockIdx.x;
       s0.slab = w0;
-      if (HYB) {
-        const uint32_t in = __ballot_sync(kFull, w0 < runs);   // the first lane: the run of slab w0
-        s0.run = in ? __ffs(in) - 1 : 0;
-        s0.slab = w0 - (__shfl_sync(kFull, runs - k, s0.run));
-      }
     }
   } else if (n_items <= kThreads) {
-    const Item it = load_item<HYB>(p, tid, n_items);
-    long long total;
-    const long long lo = scan(it.slabs, total);
+    const int slabs = item_slabs<HYB>(p, tid, n_items);
+    int total;
+    const int lo = scan(slabs, total);
     cut_ranges(total);
-    place(it, tid, lo);
-    __syncthreads();
-    s0 = s_start[warp];
+    place(slabs, tid, lo);
+    my_start();
   } else {
-    long long mine_all = 0, total = 0;
-    for (int i = tid; i < n_items; i += kThreads) mine_all += load_item<HYB>(p, i, n_items).slabs;
+    int mine_all = 0, total = 0;
+    for (int i = tid; i < n_items; i += kThreads) mine_all += item_slabs<HYB>(p, i, n_items);
     scan(mine_all, total);
     cut_ranges(total);
-    long long before = 0;
+    int before = 0;
     for (int i0 = 0; i0 < n_items && before < c1; i0 += kThreads) {
-      const Item it = load_item<HYB>(p, i0 + tid, n_items);
+      const int slabs = item_slabs<HYB>(p, i0 + tid, n_items);
       __syncthreads();   // the last round's sums were read
-      long long round;
-      const long long lo = before + scan(it.slabs, round);
-      place(it, i0 + tid, lo);
+      int round;
+      const int lo = before + scan(slabs, round);
+      place(slabs, i0 + tid, lo);
       before += round;
     }
-    __syncthreads();
-    s0 = s_start[warp];
+    my_start();
   }
   if (!HYB) {
     // sequences of no rows give zeros
@@ -929,177 +837,178 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   // ---- the warp's slabs
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::DATA;
   WarpEnd end{-1, -1, 0};
-  float* scratch = p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE;
   using Wk = Warp<T, CODE, D, G, HYB>;
   Wk wk(p, ring, smem_u32(smem) + C::OFF_AUX + warp * C::WARP_AUX);
   if (mine > 0) {
     typename Wk::RawQ raw;
     wk.fetch_q(s0.seg, raw);      // (arrives while the first slabs are on their way)
-    wk.begin(s0);
-    // does the first segment begin here?
-    bool began = s0.slab == 0;
-    if (HYB && began) began = wk.next_run(s0.seg, 0, s0.run) >= s0.run;
+    bool more = wk.begin(s0);
     int copied = 0;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (copied > 0 && copied < mine && !wk.advance()) mine = copied;
-      if (copied < mine) {
+      if (more && copied < mine) {
         wk.copy(i);
         ++copied;
+        more = wk.advance();
       }
-      cp_async_commit();
     }
     int seg = s0.seg;
     wk.set_q(seg, raw);
     wk.reset();
+    bool began = s0.slab == 0 && (!HYB || wk.first_tile(s0.seg, s0.tile));
     int si = 0, so = kStages - 1;     // the stage read next, the stage filled next
-    for (int i = 0; i < mine; ++i) {
-      cp_async_wait<kStages - 2>();
+    uint32_t phase = 0;
+    for (int i = 0; i < copied; ++i) {
+      uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX) + si;
+      if (!mbar_wait(bar, phase, p.err)) break;   // (flagged; the result is lost)
       __syncwarp();
       const uint4 hd = lds128(wk.aux + si * C::AUX + C::AUX_HEAD);
-      if (hd.y & kFullSlab) {
-        uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX + C::LIST) + si;
-        if (!mbar_wait(bar, (wk.parity >> si) & 1u, p.err)) break;   // (flagged; the result is lost)
-        wk.parity ^= 1u << si;
-      }
       if ((int)hd.x != seg) {
         if (began) wk.write_out(seg);
         else {
-          wk.write_state(scratch);
+          wk.write_state(p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE);
           end.ended = seg;
         }
         began = true;
         seg = (int)hd.x;
-        typename Wk::RawQ raw;
         wk.fetch_q(seg, raw);
         wk.set_q(seg, raw);
         wk.reset();
       }
-      if (copied < mine && !wk.advance()) mine = copied;
-      if (copied < mine) {
+      if (more && copied < mine) {
         wk.copy(so);
         ++copied;
+        more = wk.advance();
       }
-      cp_async_commit();
-      wk.consume(si, hd, seg);
-      si = si + 1 == kStages ? 0 : si + 1;
+      wk.consume(si, hd);
       so = so + 1 == kStages ? 0 : so + 1;
+      if (++si == kStages) {
+        si = 0;
+        phase ^= 1u;
+      }
       __syncwarp();   // the stage is free to be written
     }
-    // is the last segment complete?  (the cursor stands on its last copied slab)
-    bool last = wk.cur.at + 1 >= wk.cur.count;
-    if (HYB && last) last = wk.next_run(seg, wk.cur.run + 1, wk.cur.runs) >= wk.cur.runs;
-    if (p.whole) {
-      // the CTA merges the segment's states and writes it
-      end.open = seg;
-      end.began = began;
-    } else if (last && began) wk.write_out(seg);
-    else if (last) {
-      wk.write_state(scratch);
-      end.ended = seg;
-    } else {
-      end.open = seg;
-      end.began = began;
+    // is the last segment complete?  (the cursor stands on the slab after the last)
+    const bool done = !p.whole && !(more && wk.seg == seg);
+    if (done && began) wk.write_out(seg);
+    else {
+      // (an open state goes where the warp's ring was)
+      wk.write_state(done ? p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE
+                          : reinterpret_cast<float*>(smem + warp * kStages * C::DATA));
+      if (done) end.ended = seg;
+      else {
+        end.open = seg;
+        end.began = began;
+      }
     }
   }
-  if (lane == 0) {
-    s_end[warp] = end;
-    s_has[warp] = end.open >= 0;
-  }
-  __syncthreads();   // every ring is drained
-  float* states = reinterpret_cast<float*>(smem);
-  if (end.open >= 0) wk.write_state(states + warp * C::STATE);
+  if (lane == 0) s_end[warp] = end;
   __syncthreads();
 
-  // ---- merge: chains of states of one segment across the CTA's warps
+  // ---- merge.  Entry 2w is warp w's ended state (of a segment that began before the
+  // warp), entry 2w + 1 its open one.  Valid entries of one segment are neighbours:
+  // a chain.  A chain's factors first (one warp a head), then its columns.
+  if (warp < G) {
+    const WarpEnd we = lane < kEntries ? s_end[lane >> 1] : WarpEnd{-1, -1, 0};
+    const int h = warp, eseg = lane & 1 ? we.open : we.ended;
+    const bool valid = eseg >= 0;
+    float m = kNoRef, l = 0.f;
+    if (valid) {
+      const float* s = lane & 1 ? reinterpret_cast<const float*>(smem + (lane >> 1) * kStages * C::DATA)
+                                : p.scratch + ((size_t)blockIdx.x * kWarps + (lane >> 1)) * C::STATE;
+      m = s[h];
+      l = s[G + h];
+    }
+    const uint32_t vmask = __ballot_sync(kFull, valid);
+    const uint32_t below = vmask & ((1u << lane) - 1u);
+    const int prev = __shfl_sync(kFull, eseg, below ? 31 - __clz(below) : lane);
+    const uint32_t firsts = __ballot_sync(kFull, valid && (!below || prev != eseg));
+    // the chain's lanes: from its first valid entry up to the next chain's
+    const uint32_t upto = firsts & ((2u << lane) - 1u);
+    const int c0_lane = upto ? 31 - __clz(upto) : 0;
+    const uint32_t after = firsts & ~((2u << lane) - 1u);
+    const int c1_lane = after ? __ffs(after) - 2 : 31;
+    float M = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(kFull, M, o);
+      if (lane - o >= c0_lane) M = fmaxf(M, y);
+    }
+    M = __shfl_sync(kFull, M, c1_lane);
+    const float f = fast_exp2(m - M);
+    float L = f * l;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(kFull, L, o);
+      if (lane - o >= c0_lane) L += y;
+    }
+    L = __shfl_sync(kFull, L, c1_lane);
+    s_f[h][lane] = valid ? f : 0.f;
+    s_m[h][lane] = M;
+    s_l[h][lane] = L;
+    if (h == 0 && lane == 0) {
+      s_valid = vmask;
+      s_first = firsts;
+    }
+  }
+  __syncthreads();
+  const uint32_t valid = s_valid;
   int part_seg[2] = {-1, -1};
-  // every warp that has a state has one of the same open segment: the maximum
-  // first, then independent terms
-  bool single = true;
-  int sseg = -1, sbegan = 0;
+  constexpr int kQuads = G * D / 4;                          // threads a chain takes
+  constexpr int kGroups = kThreads / kQuads;                 // chains at once
+  uint32_t firsts = s_first;
+  for (int chain = 0; firsts; ++chain) {
+    const int e0 = __ffs(firsts) - 1;
+    firsts &= firsts - 1;
+    const uint32_t mine_e = valid & (firsts ? (1u << (__ffs(firsts) - 1)) - 1u : 0xffffffffu) & ~((1u << e0) - 1u);
+    const int e1 = 31 - __clz(mine_e);
+    const WarpEnd wf = s_end[e0 >> 1];
+    const int cseg = e0 & 1 ? wf.open : wf.ended;
+    const bool cbegan = (e0 & 1) && wf.began, cended = !(e1 & 1) || p.whole;
+    const int slot = cbegan && !cended ? 1 : 0;
+    const bool out = cended && (cbegan || p.whole);
+    if (!out) part_seg[slot] = cseg;
+    if (tid / kQuads != chain % kGroups) continue;
+    const int col = (tid % kQuads) * 4, h = col / D, e = col - h * D;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t left = mine_e; left;) {
+      float2 x[4], y[4];
+      float f[4];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const WarpEnd we = s_end[w];
-    if (we.ended >= 0) single = false;
-    if (we.open >= 0) {
-      if (sseg >= 0 && we.open != sseg) single = false;
-      sseg = we.open;
-      sbegan |= we.began;
-    }
-  }
-  if (single) {
-    if (sseg >= 0)
-      for (int col = tid; col < G * D; col += kThreads) {
-        const int h = col / D, e = col - h * D;
-        float m[kWarps], l = 0.f, a = 0.f, M = kNoRef;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          m[w] = s_has[w] ? states[w * C::STATE + h] : kNoRef;
-          M = fmaxf(M, m[w]);
-        }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = fast_exp2(m[w] - M);
-          if (s_has[w]) {
-            l = fmaf(f, states[w * C::STATE + G + h], l);
-            a = fmaf(f, states[w * C::STATE + 2 * G + col], a);
-          }
-        }
-        if (p.whole) {
-          const int b = sseg / p.Hkv, g = sseg - b * p.Hkv;
-          store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + e, l > 0.f ? a / l : 0.f);
-        } else {
-          float* s = p.parts + ((size_t)blockIdx.x * 2 + sbegan) * C::STATE;
-          s[2 * G + col] = a;
-          if (e == 0) {
-            s[h] = M;
-            s[G + h] = l;
-          }
+      for (int u = 0; u < 4; ++u) {
+        x[u] = y[u] = make_float2(0.f, 0.f);
+        f[u] = 0.f;
+        if (left) {
+          const int k = __ffs(left) - 1;
+          left &= left - 1;
+          const float* s = (k & 1 ? reinterpret_cast<const float*>(smem + (k >> 1) * kStages * C::DATA)
+                                  : p.scratch + ((size_t)blockIdx.x * kWarps + (k >> 1)) * C::STATE) + 2 * G + col;
+          f[u] = s_f[h][k];
+          x[u] = *reinterpret_cast<const float2*>(s);
+          y[u] = *reinterpret_cast<const float2*>(s + 2);
         }
       }
-    part_seg[sbegan] = sseg;
-  }
-  for (int col = tid; !single && col < G * D; col += kThreads) {
-    const int h = col / D, e = col - h * D;
-    Chain ch;
-    ch.clear();
-    int cseg = -1;
-    bool cbegan = false;
-    auto leave = [&](int slot) {   // an incomplete chain goes to the CTA's slot
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        a.x = fmaf(f[u], x[u].x, a.x);
+        a.y = fmaf(f[u], x[u].y, a.y);
+        a.z = fmaf(f[u], y[u].x, a.z);
+        a.w = fmaf(f[u], y[u].y, a.w);
+      }
+    }
+    const float L = s_l[h][e0];
+    if (out) {
+      const int b = cseg / p.Hkv, g = cseg - b * p.Hkv;
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      store4(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + e, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    } else {
       float* s = p.parts + ((size_t)blockIdx.x * 2 + slot) * C::STATE;
-      s[2 * G + col] = ch.a;
+      *reinterpret_cast<float2*>(s + 2 * G + col) = make_float2(a.x, a.y);
+      *reinterpret_cast<float2*>(s + 2 * G + col + 2) = make_float2(a.z, a.w);
       if (e == 0) {
-        s[h] = ch.m;
-        s[G + h] = ch.l;
+        s[h] = s_m[h][e0];
+        s[G + h] = L;
       }
-    };
-    part_seg[0] = part_seg[1] = -1;
-    for (int w = 0; w < kWarps; ++w) {
-      const WarpEnd we = s_end[w];
-      if (we.ended >= 0) {
-        const float* s = p.scratch + ((size_t)blockIdx.x * kWarps + w) * C::STATE;
-        ch.add(s[h], s[G + h], s[2 * G + col]);
-        if (cbegan) {
-          const int b = we.ended / p.Hkv, g = we.ended - b * p.Hkv;
-          store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + e, ch.l > 0.f ? ch.a / ch.l : 0.f);
-        } else {
-          leave(0);
-          part_seg[0] = we.ended;
-        }
-        ch.clear();
-        cseg = -1;
-        cbegan = false;
-      }
-      if (we.open >= 0) {
-        const float* s = states + w * C::STATE;
-        if (we.began) cbegan = true;
-        cseg = we.open;
-        ch.add(s[h], s[G + h], s[2 * G + col]);
-      }
-    }
-    if (cseg >= 0) {
-      leave(cbegan ? 1 : 0);
-      part_seg[cbegan ? 1 : 0] = cseg;
     }
   }
   if (tid == 0 && !p.whole) {
@@ -1163,45 +1072,6 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
   }
 }
 
-// ---- hybrid: slabs of every run -------------------------------------------------------------
-// A run is kQ8Run positions of one segment; its rows are those that some head of
-// the group uses: all below n_b in a group with a retrieval head, else the union
-// of the sets.  One warp a run.  Also clears the output (segments whose sets are
-// all empty have no slab and so no writer).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) q8_runs_kernel(const __grid_constant__ Q8AttnParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long all = (long long)p.B * p.Hkv * p.runs_stride;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)p.B * p.Hq * D; i += (long long)gridDim.x * 256)
-    store1(static_cast<T*>(p.out) + i, 0.f);
-  if (id >= (long long)p.n_run_items * 16) return;
-  int rows = 0;
-  if (id < all) {
-    const int seg = (int)(id / p.runs_stride), run = (int)(id - (long long)seg * p.runs_stride);
-    const int b = seg / p.Hkv, g = seg - b * p.Hkv, G = p.Hq / p.Hkv;
-    const int n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
-    const int base = run * kQ8Run, left = min(n - base, kQ8Run);
-    bool dense = false;
-    for (int t = 0; t < G; ++t) dense = dense || ((p.role[(g * G + t) >> 5] >> ((g * G + t) & 31)) & 1u);
-    if (left > 0) {
-      if (dense) rows = left;
-      else {
-        uint32_t u = 0;
-        const int w = (base >> 5) + lane;
-        if (lane < kQ8Run / 32 && 32 * w < n) {
-          for (int t = 0; t < G; ++t) u |= __ldcg(&p.bitmaps[((size_t)b * p.Hq + g * G + t) * p.nwords + w]);
-          if (n - 32 * w < 32) u &= (1u << (n - 32 * w)) - 1u;
-        }
-        rows = warp_sum_int(__popc(u));
-      }
-    }
-  }
-  if (lane == 0) p.run_slabs[id] = (uint8_t)((rows + 15) >> 4);
-}
-
 // ---- launches ----------------------------------------------------------------------------------
 template <typename T, int CODE, int D, int G, bool HYB>
 cudaError_t launch_g(const Q8AttnParams& p, int grid, cudaStream_t st) {
@@ -1227,11 +1097,7 @@ cudaError_t launch_h(const Q8AttnParams& p, int grid, cudaStream_t st) {
 
 template <typename T, int CODE, int D>
 cudaError_t launch_d(const Q8AttnParams& p, int grid, cudaStream_t st) {
-  if (!p.run_slabs) return launch_h<T, CODE, D, false>(p, grid, st);
-  const long long runs = (long long)p.n_run_items * 16;
-  if ((runs + 7) / 8 > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_pdl(q8_runs_kernel<T, D>, dim3((unsigned)((runs + 7) / 8)), dim3(256), 0, st, p);
-  return e != cudaSuccess ? e : launch_h<T, CODE, D, true>(p, grid, st);
+  return p.tile_rows ? launch_h<T, CODE, D, true>(p, grid, st) : launch_h<T, CODE, D, false>(p, grid, st);
 }
 
 template <typename T, int CODE>

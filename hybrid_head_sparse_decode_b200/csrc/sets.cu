@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kThreads) build_bits_kernel(const __grid_const
   if (threadIdx.x < 2) s_lo[threadIdx.x] = s_hi[threadIdx.x] = 0;
   __syncthreads();
   const int b = blockIdx.x / p.nheads, h = p.heads[blockIdx.x % p.nheads];
-  const int n = min(max(p.seqlens[b], p.empty_ok ? 0 : 1), p.N_max);
+  const int n = min(max(p.seqlens[b], 1), p.N_max);
   const size_t bh = (size_t)b * p.Hq + h;
   uint32_t* row = p.bitmaps + bh * p.nwords;
   const int words = (n + 31) >> 5;
