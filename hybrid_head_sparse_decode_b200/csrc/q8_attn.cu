@@ -7,22 +7,19 @@
 // (or over the head's set), out = sum_j p_j sv c'_j.  A sequence of no rows and an
 // empty set give zeros.  Both products run on the tensor cores without a second
 // rounding of the cache, and take the scales afterwards.
-//   q . c   bf16 queries on e4m3 codes: the codes are an operand as they are, and q
-//           is two e4m3 parts, hi = e4m3(q') and lo = e4m3(16 (q' - hi)) with q' = q
-//           times a power of two that brings its largest magnitude to [2^7, 2^8): the
-//           two hold a bf16 exactly above 2^-13 of the largest, and to 2^-21 of the
-//           largest below.  Otherwise codes become halves (exact: both code types
-//           fit 11 bits), q' has its largest magnitude in [2^13, 2^14), and fp32
-//           queries are held in two halves (22 bits).
-//   p . c'  codes become halves.  The weight that multiplies them is w_j = p_j sv_j;
-//           it is what must fit a half, so the running reference of the online
-//           softmax is the maximum of s_j log2(e) + log2(sv_j), and the normaliser
-//           sums w_j / sv_j beside it.  The reference is kept 6 below the maximum
-//           seen and moved only when a weight would pass 2^15: weights down to 2^-31
-//           of the largest keep a place in the half's range (an 8-bit float's range
-//           would lose the many small weights of a long context).  With bf16
-//           queries a weight is rounded to 11 bits (the output has 8); with fp32
-//           ones it is held in two halves.
+// The codes become halves (exact: both code types fit 11 bits); the 8-bit forms of
+// mma.sync are no use here, the compiler turns them into the same conversions and
+// more (a slab then took 490 instructions against 330).  q is scaled by a power of
+// two that brings its largest magnitude to [2^13, 2^14): a bf16 is then a half
+// exactly down to 2^-27 of the largest, and an fp32 is held in two halves (22
+// bits).  The weight that multiplies the values' codes is w_j = p_j sv_j; it is what
+// must fit a half, so the running reference of the online softmax is the maximum
+// of s_j log2(e) + log2(sv_j), and the normaliser sums w_j / sv_j beside it.  The
+// reference is kept 6 below the maximum seen and moved only when a weight would
+// pass 2^15: weights down to 2^-31 of the largest keep a place in the half's range
+// (an 8-bit float's range would lose the many small weights of a long context).
+// With bf16 queries a weight is rounded to 11 bits (the output has 8); with fp32
+// ones it is held in two halves.
 //
 // Work split.  The unit is a slab of 16 rows of one KV head.  All slabs of the
 // call, ordered by sequence, head and position, are cut into one equal range per
@@ -40,10 +37,9 @@
 // segment is one CTA's and nothing is left to merge.  All sums have a fixed order.
 //
 // Layouts.  Rows lie in shared memory with the TMA's swizzle (16-byte pieces of a
-// row XORed with its number).  S = K q^T as m16n8k32 (e4m3) or m16n8k16 (halves)
-// with the slab's rows as M: a lane takes 16-byte piece c (c = lane % 4) of its
+// row XORed with its number).  S = K q^T as m16n8k16 with the slab's rows as M: a lane takes 16-byte piece c (c = lane % 4) of its
 // two rows; which dimension a k index means is free as long as q agrees, so a
-// row's words are, or convert to, A fragments in place.  O^T = V^T P with the
+// row's words convert to A fragments in place.  O^T = V^T P with the
 // dimensions as M: a lane takes piece lane / 4 of four rows; interleaving the bytes
 // of two rows gives the pairs along k that A wants.  Which row stands at which index
 // of M and k is free too: index i is row i ^ 4 (i & 1), which makes both reads
@@ -125,13 +121,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-               "{%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -143,14 +132,6 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 }
 __device__ __forceinline__ float2 unpack_half(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-// Four values -> four e4m3 codes (NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 template <typename T>
@@ -177,11 +158,9 @@ __device__ __forceinline__ void store4(float* p, float a, float b, float c, floa
 
 template <typename T, int CODE, int D, int G>
 struct Cfg {
-  static constexpr bool kF8 = sizeof(T) == 2 && CODE == kCodeE4M3;   // q as two e4m3 parts
   static constexpr bool kTwo = sizeof(T) == 4;           // q and the weights in two halves
   static constexpr bool kBeside = kTwo && G <= 4;        // ... in columns 0-3 and 4-7 of one product
-  static constexpr int NQ = (kTwo && !kBeside) || kF8 ? 2 : 1;   // products of S per k step
-  static constexpr int KQ = kF8 ? D / 32 : D / 16;       // k steps of S
+  static constexpr int NQ = kTwo && !kBeside ? 2 : 1;    // ... or in two products
   static constexpr int KM = D / 16;                      // blocks of 16 dimensions of O
   static constexpr int H = D / 64;                       // 16-byte pieces of K a lane takes of a row
   static constexpr int VB = D / 8;                       // bytes of V a lane takes of each of its four rows
@@ -406,7 +385,7 @@ struct Warp {
   }
 
   // ---- the heads' states
-  uint32_t qf[C::NQ][C::KQ][2];   // q as B fragments
+  uint32_t qf[C::NQ][C::KM][2];   // q as B fragments
   float fq[2];                    // powers of two that undo q's scaling, of this lane's two columns
   float ref[2], l[2];             // reference (log2) and sum of p, of this lane's two columns
   float acc[C::KM][4];
@@ -447,23 +426,11 @@ struct Warp {
       mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x[m].x), fabsf(x[m].y)), fmaxf(fabsf(x[m].z), fabsf(x[m].w))));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    // the largest magnitude to [2^top, 2^(top + 1)) (below 2^-100 the same factor as at 2^-100)
-    constexpr int top = C::kF8 ? 7 : 13;
+    // the largest magnitude to [2^13, 2^14) (below 2^-100 the same factor as at 2^-100)
+    constexpr int top = 13;
     const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
     const float up = exp2_int(top - e);
     const float down = mx < INFINITY ? exp2_int(e - top) : NAN;   // (an infinite q has no score)
-    if constexpr (C::kF8) {
-      // x[m] holds four dimensions: two m to a k step of 32
-#pragma unroll
-      for (int m = 0; m < C::KM; ++m) {
-        const float a[4] = {x[m].x * up, x[m].y * up, x[m].z * up, x[m].w * up};
-        const uint32_t hi = e4m3x4(a[0], a[1], a[2], a[3]);
-        const float4 h = codes_to_float<kCodeE4M3>(hi);
-        qf[0][m >> 1][m & 1] = hi;
-        qf[C::NQ - 1][m >> 1][m & 1] =
-            e4m3x4(16.f * (a[0] - h.x), 16.f * (a[1] - h.y), 16.f * (a[2] - h.z), 16.f * (a[3] - h.w));
-      }
-    } else {
 #pragma unroll
     for (int m = 0; m < C::KM; ++m) {
       const float a = x[m].x * up, bb = x[m].y * up, cc = x[m].z * up, d = x[m].w * up;
@@ -481,7 +448,6 @@ struct Warp {
       }
       qf[0][m][0] = w0;
       qf[0][m][1] = w1;
-    }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) fq[j] = __shfl_sync(kFull, down, (column_head(j) & 7) * 4);
@@ -504,14 +470,6 @@ struct Warp {
     for (int h = 0; h < C::H; ++h) {
       const uint4 lo = lds128(ka ^ (h << 6)), hi = lds128((ka ^ (h << 6)) + 8 * D);
       const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-      if constexpr (C::kF8) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int m = h * 2 + j;
-          mma_e4m3(s, wl[2 * j], wh[2 * j], wl[2 * j + 1], wh[2 * j + 1], qf[0][m][0], qf[0][m][1]);
-          mma_e4m3(s2, wl[2 * j], wh[2 * j], wl[2 * j + 1], wh[2 * j + 1], qf[C::NQ - 1][m][0], qf[C::NQ - 1][m][1]);
-        }
-      } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int m = h * 4 + j;
@@ -519,12 +477,11 @@ struct Warp {
           codes_to_half<CODE>(wl[j], a0, a2);
           codes_to_half<CODE>(wh[j], a1, a3);
           mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[0][m][0], qf[0][m][1]);
-          if constexpr (C::NQ == 2) mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[C::NQ - 1][m][0], qf[C::NQ - 1][m][1]);
+          if constexpr (C::NQ == 2) mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[1][m][0], qf[1][m][1]);
         }
-      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = C::kF8 ? fmaf(s2[i], 0.0625f, s[i]) : s[i] + s2[i];
+    for (int i = 0; i < 4; ++i) s[i] += s2[i];
     if (C::kBeside) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(kFull, s[i], 2);
