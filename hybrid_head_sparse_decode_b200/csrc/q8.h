@@ -34,9 +34,11 @@ struct Q8AppendParams {
 cudaError_t launch_q8_append(const Q8AppendParams& p, int dtype, int code, int D, cudaStream_t st);
 
 // Attention of one query token a sequence over the cache (q8_attn.cu).
-constexpr int kQ8Warps = 16;       // warps of an attention CTA (one CTA an SM)
+constexpr int kQ8Warps = 12;       // warps of an attention CTA (one CTA an SM)
+constexpr int kQ8Stages = 2;       // slabs in a warp's ring
+constexpr int kQ8Slab = 32;        // rows of a slab
 constexpr int kQ8MaxCtas = 160;    // attention CTAs at most (the workspace holds that many states)
-constexpr int kQ8MinSlabs = 2;     // slabs of 16 rows a warp takes at least, while there are any
+constexpr int kQ8MinSlabs = 1;     // slabs a warp takes at least, while there are any
 constexpr int kQ8WholeMax = 1024;  // positions of a segment that one CTA takes alone, at most
 constexpr int kQ8Tile = 4096;      // positions of a tile (hybrid: the unit whose rows are listed)
 struct Q8AttnParams {
@@ -63,7 +65,7 @@ struct Q8AttnParams {
   const int32_t* k_per_seq;  // [B] or null (checked here)
   int nwords, ntiles, k, n_sparse;
   int whole;                 // 1: CTA x takes segment x whole, nothing is left open
-  // the cache's codes as rows of D bytes, boxes of sixteen rows, swizzled by D bytes
+  // the cache's codes as rows of D bytes, boxes of 32 rows (pages of 16: 16 rows), swizzled by D bytes
   alignas(64) CUtensorMap tmk;
   alignas(64) CUtensorMap tmv;
 };

@@ -30,9 +30,9 @@ lychee_status check_q8_shape(const lychee_q8_shape* s) {
   // rows are counted in 32 bits
   if ((long long)s->num_pages * s->Hkv * s->page > 0x7fffffffLL) return LYCHEE_ERR_UNSUPPORTED;
   if ((long long)s->B * s->Hq >= (1LL << 24)) return LYCHEE_ERR_UNSUPPORTED;
-  // slabs of 16 rows, over all sequences and heads, are counted in 32 bits too
+  // slabs, over all sequences and heads, are counted in 32 bits too
   const long long n_max = (long long)s->max_pages * s->page;
-  if ((long long)s->B * s->Hkv * ((n_max + kQ8Tile - 1) / kQ8Tile) * (kQ8Tile / 16) > 0x7fffffffLL)
+  if ((long long)s->B * s->Hkv * ((n_max + kQ8Tile - 1) / kQ8Tile) * (kQ8Tile / kQ8Slab) > 0x7fffffffLL)
     return LYCHEE_ERR_UNSUPPORTED;
   return LYCHEE_OK;
 }
@@ -105,7 +105,8 @@ lychee_status check_sets(const lychee_q8_shape* s, int k, int block) {
   return LYCHEE_OK;
 }
 
-// The codes of a cache as an array of rows of d bytes, in boxes of sixteen rows
+// The codes of a cache as an array of rows of d bytes, in boxes of 32 rows (16 when a
+// page has no more)
 // whose 16-byte pieces are swizzled over 128 (d = 64: 64) bytes.  False when the
 // driver offers no encoder or refuses the map.
 bool encode_rows(CUtensorMap* m, const void* base, const lychee_q8_shape* s) {
@@ -113,7 +114,7 @@ bool encode_rows(CUtensorMap* m, const void* base, const lychee_q8_shape* s) {
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)s->d, (cuuint64_t)s->num_pages * s->Hkv * s->page};
   const cuuint64_t strides[1] = {(cuuint64_t)s->d};
-  const cuuint32_t box[2] = {(cuuint32_t)s->d, 16u};
+  const cuuint32_t box[2] = {(cuuint32_t)s->d, s->page == 16 ? 16u : 32u};
   const cuuint32_t estr[2] = {1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, s->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,

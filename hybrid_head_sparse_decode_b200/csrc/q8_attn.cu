@@ -21,14 +21,14 @@
 // With bf16 queries a weight is rounded to 11 bits (the output has 8); with fp32
 // ones it is held in two halves.
 //
-// Work split.  The unit is a slab of 16 rows of one KV head.  All slabs of the
+// Work split.  The unit is a slab of 32 rows of one KV head.  All slabs of the
 // call, ordered by sequence, head and position, are cut into one equal range per
 // CTA and that into one per warp, whatever the lengths (a sequence's and a head's
 // slabs are a segment; a hybrid layer counts only the rows that some head of the
 // group uses).  A warp works alone: it brings its slabs into a ring of its own in
 // shared memory and runs the G heads of the group over each slab at once; no
-// barrier joins the warps before the end.  A full slab is 16 consecutive rows of
-// one page: two TMA boxes (K and V).  The rows of a sparse head's set, and a
+// barrier joins the warps before the end.  A full slab is 32 consecutive rows: a
+// TMA box of K and one of V (two each when pages have 16 rows).  The rows of a sparse head's set, and a
 // slab cut by the sequence's end, come row by row (cp.async, absent rows as
 // zeros).  At the end the CTA merges its warps' states of a segment, writes what
 // is complete and leaves at most two states open: of a segment that began in an
@@ -37,7 +37,7 @@
 // segment is one CTA's and nothing is left to merge.  All sums have a fixed order.
 //
 // Layouts.  Rows lie in shared memory with the TMA's swizzle (16-byte pieces of a
-// row XORed with its number).  S = K q^T as m16n8k16 with the slab's rows as M: a lane takes 16-byte piece c (c = lane % 4) of its
+// row XORed with its number).  S = K q^T as m16n8k16 with 16 of the slab's rows as M: a lane takes 16-byte piece c (c = lane % 4) of its
 // two rows; which dimension a k index means is free as long as q agrees, so a
 // row's words convert to A fragments in place.  O^T = V^T P with the
 // dimensions as M: a lane takes piece lane / 4 of four rows; interleaving the bytes
@@ -55,7 +55,8 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = kQ8Warps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kStages = kQ8Stages;
+constexpr int kRows = kQ8Slab;       // rows of a slab: two halves of 16, the M of the products
 constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
 constexpr float kRefSlack = 15.f;    // and moves when a weight passes it by more than this
 constexpr uint32_t kAbsent = 0xffffffffu;  // of a slab's rows: none
@@ -116,7 +117,7 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                "{%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -164,11 +165,12 @@ struct Cfg {
   static constexpr int KM = D / 16;                      // blocks of 16 dimensions of O
   static constexpr int H = D / 64;                       // 16-byte pieces of K a lane takes of a row
   static constexpr int VB = D / 8;                       // bytes of V a lane takes of each of its four rows
-  static constexpr int DATA = 32 * D;                    // a stage's rows: K, then V
-  static constexpr int OFF_V = 16 * D;
-  // beside the rows, per stage: row scales (K's, V's), the rows each head uses
-  // (u16 a head), the header {segment, position | flags, K scale, V scale}
-  static constexpr int AUX_S = 0, AUX_META = 128, AUX_HEAD = 144, AUX = 160;
+  static constexpr int DATA = 2 * kRows * D;             // a stage's rows: K, then V
+  static constexpr int OFF_V = kRows * D;
+  // beside the rows, per stage: row scales (K's, V's; of a full slab one per half:
+  // K's, V's), the rows each head uses (a word a head), the header {segment, position
+  // | flags}
+  static constexpr int AUX_S = 0, AUX_META = 256, AUX_HEAD = 288, AUX = 304;
   static constexpr int WARP_AUX = kStages * AUX + 32;    // and the stages' mbarriers
   static constexpr int OFF_AUX = kWarps * kStages * DATA;
   static constexpr int STATE = G * (D + 2);              // floats of a state: m[G], l[G], acc[G][D]
@@ -190,6 +192,7 @@ struct Warp {
   uint32_t ring, aux, bars;
   int lane, r, c;
   uint32_t gathered;    // bit i: stage i was last filled row by row
+  uint32_t kofs, vofs_a, vofs_b;   // this lane's pieces in a stage: K of row R, V of rows Ra and Rb
 
   // The warp's place in its slabs: the next one to copy.
   int seg, b, g, n;
@@ -205,6 +208,10 @@ struct Warp {
     r = lane >> 2;
     c = lane & 3;
     gathered = 0;
+    const int R = r ^ ((r & 1) << 2), Ra = 2 * c, Rb = (2 * c) ^ 5;
+    kofs = R * D + ((D == 128 ? c ^ (R & 7) : c ^ ((R >> 1) & 3)) << 4);
+    vofs_a = C::OFF_V + Ra * D + (D == 128 ? (r ^ (Ra & 7)) << 4 : (((r >> 1) ^ ((Ra >> 1) & 3)) << 4) + (r & 1) * 8);
+    vofs_b = C::OFF_V + Rb * D + (D == 128 ? (r ^ (Rb & 7)) << 4 : (((r >> 1) ^ ((Rb >> 1) & 3)) << 4) + (r & 1) * 8);
     tile = 0;
     sparse = mixed = false;
     if (lane == 0) {
@@ -263,7 +270,7 @@ struct Warp {
   // Start loading what the slab at the cursor needs.
   __device__ __forceinline__ void preload() {
     if (HYB && sparse) {
-      const int e = 16 * at + (lane & 15);
+      const int e = kRows * at + lane;
       const size_t from = ((size_t)seg * p.ntiles + tile) * kQ8Tile + e;
       pre = kAbsent;
       pre_m = 0;
@@ -272,13 +279,13 @@ struct Warp {
         pre_m = __ldcg(p.list_heads + from);
       }
     } else {
-      const int pos0 = tile * kQ8Tile + 16 * at;
-      pre = __ldg(&p.c.table[(size_t)b * p.c.max_pages + (pos0 >> p.c.page_log2)]);
+      // (a page of 16 positions is half a slab: odd lanes take the second half's)
+      const int pos0 = tile * kQ8Tile + kRows * at, pos = pos0 + 16 * (lane & 1);
+      pre = __ldg(&p.c.table[(size_t)b * p.c.max_pages + ((pos < n ? pos : pos0) >> p.c.page_log2)]);
       if (HYB && mixed) {
-        pre_m = 0xffffu;
+        pre_m = 0xffffffffu;
         if (lane < G && !retrieval(g * G + lane))
-          pre_m = __ldcg(reinterpret_cast<const uint16_t*>(p.bitmaps) +
-                         ((size_t)b * p.Hq + g * G + lane) * p.nwords * 2 + (pos0 >> 4));
+          pre_m = __ldcg(p.bitmaps + ((size_t)b * p.Hq + g * G + lane) * p.nwords + (pos0 >> 5));
       }
     }
   }
@@ -292,7 +299,7 @@ struct Warp {
   }
   // To the next slab; false: there is none.
   __device__ __forceinline__ bool advance() {
-    if (16 * ++at >= rows) {
+    if (kRows * ++at >= rows) {
       if (HYB) {
         if (!enter_tile(tile + 1)) {
           do {
@@ -317,51 +324,61 @@ struct Warp {
   __device__ __forceinline__ void copy(int si) {
     const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX, bar = bars + 8 * si;
     const int log2p = p.c.page_log2;
-    const int i = lane & 15;
     uint32_t myrow, heads, flags = 0;     // this lane's row; lane t: the rows head t uses
     if (!HYB || !sparse) {
-      // consecutive positions, all in one page (pages are whole slabs)
-      const int pos0 = tile * kQ8Tile + 16 * at;
-      const bool ok = pre < (uint32_t)p.c.num_pages;
-      if (!ok && lane == 0) flag_error(p.err, kErrBadIndex);
+      // consecutive positions: a half lies in one page
+      const int pos0 = tile * kQ8Tile + kRows * at;
+      const int rest = min(n - pos0, kRows);
+      const bool ok = pre < (uint32_t)p.c.num_pages;      // of this lane's half
+      if (!ok && lane < 2 && 16 * lane < rest) flag_error(p.err, kErrBadIndex);
       const int unit = (int)pre * p.Hkv + g;
-      const uint32_t row0 = ((uint32_t)unit << log2p) + (pos0 & ((1 << log2p) - 1));
-      const int left = ok ? n - pos0 : 0;
+      const uint32_t row0 = ((uint32_t)unit << log2p) + ((pos0 + 16 * (lane & 1)) & ((1 << log2p) - 1));
       flags = (uint32_t)pos0;
-      if (left >= 16) {
+      if (rest == kRows && __all_sync(kFull, ok)) {
+        if (lane < 2) {
+          copy4(ax + C::AUX_S + 8 * lane, p.c.k_scale + unit);      // the halves' scales
+          copy4(ax + C::AUX_S + 8 * lane + 4, p.c.v_scale + unit);
+          asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        }
+        const uint32_t row1 = __shfl_sync(kFull, row0, 1);          // (joins the lanes, too)
         if (lane == 0) {
           if ((gathered >> si) & 1u) fence_proxy_async_smem();   // ordinary writes before the TMA's
           sts64(ax + C::AUX_HEAD, (uint32_t)seg, flags | kFullSlab | (HYB && mixed ? 0u : kAllHeads));
-          copy4(ax + C::AUX_HEAD + 8, p.c.k_scale + unit);       // the block's two scales
-          copy4(ax + C::AUX_HEAD + 12, p.c.v_scale + unit);
-          asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
           asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((uint32_t)C::DATA)
                        : "memory");
           const uint64_t policy = l2_evict_first_policy();
           tma_rows(st, &p.tmk, (int)row0, bar, policy);
           tma_rows(st + C::OFF_V, &p.tmv, (int)row0, bar, policy);
+          if (log2p == 4) {   // (boxes of 16 rows; else of 32)
+            tma_rows(st + 16 * D, &p.tmk, (int)row1, bar, policy);
+            tma_rows(st + C::OFF_V + 16 * D, &p.tmv, (int)row1, bar, policy);
+          }
         }
-        if (HYB && mixed && lane < G) sts16(ax + C::AUX_META + 2 * lane, pre_m);
+        if (HYB && mixed && lane < G) sts_u(ax + C::AUX_META + 4 * lane, pre_m);
         gathered &= ~(1u << si);
         return;
       }
-      myrow = i < left ? row0 + i : kAbsent;
-      heads = ((1u << max(left, 0)) - 1u) & (HYB && mixed ? pre_m : 0xffffu);
+      // lane i: row i
+      const uint32_t half0 = __shfl_sync(kFull, row0, 0), half1 = __shfl_sync(kFull, row0, 1);
+      const uint32_t oks = __ballot_sync(kFull, ok);
+      const bool in = lane < rest && ((oks >> (lane >> 4)) & 1u);
+      myrow = in ? (lane < 16 ? half0 : half1) + (lane & 15) : kAbsent;
+      heads = __ballot_sync(kFull, in) & (HYB && mixed ? pre_m : 0xffffffffu);
     } else {
       myrow = pre;
       heads = 0;
 #pragma unroll
       for (int t = 0; t < G; ++t) {
-        const uint32_t m = __ballot_sync(kFull, lane < 16 && ((pre_m >> t) & 1u));
+        const uint32_t m = __ballot_sync(kFull, (pre_m >> t) & 1u);
         if (lane == t) heads = m;
       }
     }
-    // row by row; lane i (and i + 16) knows row i.  Absent rows are zeros with scale 1.
+    // row by row.  Absent rows are zeros with scale 1.
     gathered |= 1u << si;
     constexpr int LPR = D / 16, RPI = 32 / LPR;   // lanes a row, rows an instruction
     const int lr = lane / LPR, q = lane % LPR;
 #pragma unroll
-    for (int j = 0; j < 16 / RPI; ++j) {
+    for (int j = 0; j < kRows / RPI; ++j) {
       const int R = RPI * j + lr;
       const uint32_t row = __shfl_sync(kFull, myrow, R);
       const uint32_t dst = st + R * D + ((D == 128 ? q ^ (R & 7) : q ^ ((R >> 1) & 3)) << 4);
@@ -374,9 +391,14 @@ struct Warp {
         sts128(dst + C::OFF_V, 0u, 0u, 0u, 0u);
       }
     }
-    if (myrow != kAbsent) copy4(ax + C::AUX_S + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + (myrow >> log2p));
-    else sts_u(ax + C::AUX_S + lane * 4, __float_as_uint(1.f));
-    if (lane < G) sts16(ax + C::AUX_META + 2 * lane, heads);
+    if (myrow != kAbsent) {
+      copy4(ax + C::AUX_S + lane * 4, p.c.k_scale + (myrow >> log2p));
+      copy4(ax + C::AUX_S + 128 + lane * 4, p.c.v_scale + (myrow >> log2p));
+    } else {
+      sts_u(ax + C::AUX_S + lane * 4, __float_as_uint(1.f));
+      sts_u(ax + C::AUX_S + 128 + lane * 4, __float_as_uint(1.f));
+    }
+    if (lane < G) sts_u(ax + C::AUX_META + 4 * lane, heads);
     if (lane == 0) sts64(ax + C::AUX_HEAD, (uint32_t)seg, flags);
     // the phase ends when every lane's copies have landed
     asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -460,137 +482,160 @@ struct Warp {
   }
 
   // ---- one slab: stage `si`, its header in hd
-  __device__ __forceinline__ void consume(int si, uint4 hd) {
+  __device__ __forceinline__ void consume(int si, uint2 hd) {
     const uint32_t st = ring + si * C::DATA, ax = aux + si * C::AUX;
-    const int R = r ^ ((r & 1) << 2);      // this lane's rows of S: R and R + 8
-    // ---- S
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t ka = st + R * D + ((D == 128 ? c ^ (R & 7) : c ^ ((R >> 1) & 3)) << 4);
+    const int R = r ^ ((r & 1) << 2);      // this lane's rows of S in a half: R and R + 8
+    // ---- S of both halves
+    float s[2][4];
 #pragma unroll
-    for (int h = 0; h < C::H; ++h) {
-      const uint4 lo = lds128(ka ^ (h << 6)), hi = lds128((ka ^ (h << 6)) + 8 * D);
-      const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    for (int a = 0; a < 2; ++a) {
+      float s2[4] = {0.f, 0.f, 0.f, 0.f};
+      s[a][0] = s[a][1] = s[a][2] = s[a][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < C::H; ++h) {
+        const uint32_t at = (st + kofs + a * 16 * D) ^ (h << 6);
+        const uint4 lo = lds128(at), hi = lds128(at + 8 * D);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int m = h * 4 + j;
           uint32_t a0, a1, a2, a3;
           codes_to_half<CODE>(wl[j], a0, a2);
           codes_to_half<CODE>(wh[j], a1, a3);
-          mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[0][m][0], qf[0][m][1]);
-          if constexpr (C::NQ == 2) mma_f16((j & 1) ? s2 : s, a0, a1, a2, a3, qf[1][m][0], qf[1][m][1]);
+          mma_f16((j & 1) ? s2 : s[a], a0, a1, a2, a3, qf[0][m][0], qf[0][m][1]);
+          if constexpr (C::NQ == 2) mma_f16((j & 1) ? s2 : s[a], a0, a1, a2, a3, qf[1][m][0], qf[1][m][1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[a][i] += s2[i];
+      if (C::kBeside) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[a][i] += __shfl_xor_sync(kFull, s[a][i], 2);
+      }
+    }
+    // s[a][0], s[a][1]: row 16 a + R, columns 2c and 2c + 1; s[a][2], s[a][3]: row 16 a + R + 8
+    float sk[2][2], lv[2][2], inv[2][2];   // [half][row]: K scale, log2 and reciprocal of V scale
+    if (hd.y & kFullSlab) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const uint2 x = lds64(ax + C::AUX_S + 8 * a);
+        sk[a][0] = sk[a][1] = __uint_as_float(x.x);
+        lv[a][0] = lv[a][1] = fast_log2(__uint_as_float(x.y));
+        inv[a][0] = inv[a][1] = fast_exp2(-lv[a][0]);
+      }
+    } else {
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sk[a][i] = lds_f(ax + C::AUX_S + (R + 8 * i + 16 * a) * 4);
+          lv[a][i] = fast_log2(lds_f(ax + C::AUX_S + 128 + (R + 8 * i + 16 * a) * 4));
+          inv[a][i] = fast_exp2(-lv[a][i]);
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] += s2[i];
-    if (C::kBeside) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(kFull, s[i], 2);
+    // bit 16 a + 8 i: this lane's row counts for column j's head
+    uint32_t used[2] = {0xffffffffu, 0xffffffffu};
+    if (!(hd.y & kAllHeads)) {
+      const uint2 x = lds64(ax + C::AUX_META + 4 * column_head(0));
+      used[0] = x.x >> R;
+      used[1] = x.y >> R;
     }
-    // s[0], s[1]: row R, columns 2c and 2c + 1; s[2], s[3]: row R + 8
-    float sk[2], sv[2];
-    sk[0] = sk[1] = __uint_as_float(hd.z);
-    sv[0] = sv[1] = __uint_as_float(hd.w);
-    if (!(hd.y & kFullSlab)) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sk[i] = lds_f(ax + C::AUX_S + (R + 8 * i) * 4);
-        sv[i] = lds_f(ax + C::AUX_S + (16 + R + 8 * i) * 4);
-      }
-    }
-    const float lv[2] = {fast_log2(sv[0]), fast_log2(sv[1])};
-    const float inv[2] = {fast_exp2(-lv[0]), fast_exp2(-lv[1])};
-    // bit 16 j + R + 8 i: row R + 8 i counts for column j's head
-    uint32_t used = 0xffffffffu;
-    if (!(hd.y & kAllHeads)) used = lds_u(ax + C::AUX_META + 2 * column_head(0)) >> R;
     // t: log2 of a row's weight times its scale, -inf where a head does not use it.
     // (Columns beyond the group's heads hold zero queries; nothing reads them.)
-    float t[4];
-    bool over = false;
+    float t[2][4];
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        s[2 * i + j] *= sk[i] * fq[j];
-        const bool on = (used >> (16 * j + 8 * i)) & 1u;
-        t[2 * i + j] = on ? fmaf(s[2 * i + j], p.scale_log2, lv[i]) : -INFINITY;
-        over = over || t[2 * i + j] > ref[j] + kRefSlack;
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[a][2 * i + j] *= sk[a][i] * fq[j];
+          const bool on = (used[j] >> (16 * a + 8 * i)) & 1u;
+          t[a][2 * i + j] = on ? fmaf(s[a][2 * i + j], p.scale_log2, lv[a][i]) : -INFINITY;
+          top[j] = fmaxf(top[j], t[a][2 * i + j]);
+        }
     if (HYB && retrieves) {
       // (a group with a retrieval head has consecutive rows)
       float* out = p.logits + logit_row + ((hd.y & 0xffffffu) + R);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
+        if ((logit_cols >> j) & 1) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (((logit_cols >> j) & 1) && ((used >> (16 * j + 8 * i)) & 1u)) out[(size_t)j * p.N_max + 8 * i] = s[2 * i + j];
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if ((used[j] >> (16 * a + 8 * i)) & 1u) out[(size_t)j * p.N_max + 16 * a + 8 * i] = s[a][2 * i + j];
+        }
     }
-    if (__any_sync(kFull, over)) {
+    if (__any_sync(kFull, top[0] > ref[0] + kRefSlack || top[1] > ref[1] + kRefSlack)) {
+      float f[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mx = fmaxf(t[j], t[2 + j]);
+        float mx = top[j];
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-        if (mx > ref[j] + kRefSlack) {
-          const float to = mx - kRefBelow;
-          const float f = fast_exp2(ref[j] - to);   // 0 from kNoRef
-          l[j] *= f;
+        const float to = mx > ref[j] + kRefSlack ? mx - kRefBelow : ref[j];
+        f[j] = fast_exp2(ref[j] - to);   // 0 from kNoRef
+        l[j] *= f[j];
+        ref[j] = to;
+      }
 #pragma unroll
-          for (int m = 0; m < C::KM; ++m) {
-            acc[m][j] *= f;
-            acc[m][2 + j] *= f;
-          }
-          ref[j] = to;
+      for (int m = 0; m < C::KM; ++m) {
+        acc[m][0] *= f[0];
+        acc[m][1] *= f[1];
+        acc[m][2] *= f[0];
+        acc[m][3] *= f[1];
+      }
+    }
+    // weights, their sums without the scales, and the weights as B
+    uint32_t pb[2][C::kTwo && !C::kBeside ? 2 : 1][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          w[j] = fast_exp2(t[a][2 * i + j] - ref[j]);
+          l[j] = fmaf(w[j], inv[a][i], l[j]);
+        }
+        uint32_t hi = pack_half(w[0], w[1]);
+        if constexpr (C::kTwo) {
+          const float2 hf = unpack_half(hi);
+          const uint32_t lo = pack_half(w[0] - hf.x, w[1] - hf.y);
+          if constexpr (!C::kBeside) pb[a][1][i] = movmatrix_trans(lo);
+          else if (c >= 2) hi = lo;
+        }
+        pb[a][0][i] = movmatrix_trans(hi);
+      }
+    // ---- O: k indices 2c, 2c + 1, 2c + 8, 2c + 9 of a half are rows Ra, Rb, Ra + 8, Rb + 8
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      uint32_t v[4][C::VB / 4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = st + ((j & 1) ? vofs_b : vofs_a) + (16 * a + (j >> 1) * 8) * D;
+        if constexpr (D == 128) {
+          const uint4 x = lds128(at);
+          v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+        } else {
+          const uint2 x = lds64(at);
+          v[j][0] = x.x; v[j][1] = x.y;
         }
       }
-    }
-    // weights, and their sums without the scales
-    float w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < C::VB / 4; ++k) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        w[2 * i + j] = fast_exp2(t[2 * i + j] - ref[j]);
-        l[j] = fmaf(w[2 * i + j], inv[i], l[j]);
-      }
-    }
-    uint32_t pb[C::kTwo && !C::kBeside ? 2 : 1][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
-      if constexpr (C::kTwo) {
-        const float2 hf = unpack_half(hi);
-        const uint32_t lo = pack_half(w[2 * i] - hf.x, w[2 * i + 1] - hf.y);
-        if constexpr (!C::kBeside) pb[1][i] = movmatrix_trans(lo);
-        else if (c >= 2) hi = lo;
-      }
-      pb[0][i] = movmatrix_trans(hi);
-    }
-    // ---- O: rows Ra, Rb (k indices 2c, 2c + 1), Ra + 8, Rb + 8
-    const int Ra = 2 * c, Rb = (2 * c) ^ 5;
-    const uint32_t vs = st + C::OFF_V;
-    uint32_t v[4][C::VB / 4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int Rv = (j & 1) ? Rb : Ra;
-      if constexpr (D == 128) {
-        const uint4 x = lds128(vs + Rv * D + ((r ^ (Rv & 7)) << 4) + (j >> 1) * 8 * D);
-        v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-      } else {
-        const uint2 x = lds64(vs + Rv * D + (((r >> 1) ^ ((Rv >> 1) & 3)) << 4) + (r & 1) * 8 + (j >> 1) * 8 * D);
-        v[j][0] = x.x; v[j][1] = x.y;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < C::VB / 4; ++k) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t sel = half ? 0x7362u : 0x5140u;
-        uint32_t a0, a1, a2, a3;
-        codes_to_half<CODE>(__byte_perm(v[0][k], v[1][k], sel), a0, a1);
-        codes_to_half<CODE>(__byte_perm(v[2][k], v[3][k], sel), a2, a3);
-        mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[0][0], pb[0][1]);
-        if constexpr (C::kTwo && !C::kBeside) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[1][0], pb[1][1]);
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t sel = half ? 0x7362u : 0x5140u;
+          uint32_t a0, a1, a2, a3;
+          codes_to_half<CODE>(__byte_perm(v[0][k], v[1][k], sel), a0, a1);
+          codes_to_half<CODE>(__byte_perm(v[2][k], v[3][k], sel), a2, a3);
+          mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[a][0][0], pb[a][0][1]);
+          if constexpr (C::kTwo && !C::kBeside) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[a][1][0], pb[a][1][1]);
+        }
       }
     }
   }
@@ -667,8 +712,8 @@ struct Chain {
 template <bool HYB>
 __device__ __forceinline__ int item_slabs(const Q8AttnParams& p, int i, int n_items) {
   if (i >= n_items) return 0;
-  if (HYB) return (__ldcg(&p.tile_rows[i]) + 15) >> 4;
-  return ((min(max(__ldg(&p.seqlens[i]), 0), p.N_max) + 15) >> 4) * p.Hkv;
+  if (HYB) return (__ldcg(&p.tile_rows[i]) + kRows - 1) / kRows;
+  return (min(max(__ldg(&p.seqlens[i]), 0), p.N_max) + kRows - 1) / kRows * p.Hkv;
 }
 // Slab `rel` of item i, which has `slabs`.
 template <bool HYB>
@@ -757,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     if ((int)blockIdx.x < p.B * p.Hkv) {
       // (hybrid: it has one tile, its rows below kQ8WholeMax)
       const int rows = HYB ? __ldcg(&p.tile_rows[blockIdx.x]) : min(max(__ldg(&p.seqlens[blockIdx.x / p.Hkv]), 0), p.N_max);
-      const int total = (rows + 15) >> 4, per = (total + kWarps - 1) / kWarps, w0 = min(total, per * warp);
+      const int total = (rows + kRows - 1) / kRows, per = (total + kWarps - 1) / kWarps, w0 = min(total, per * warp);
       mine = min(total, w0 + per) - w0;
       s0.seg = blockIdx.x;
       s0.slab = w0;
@@ -819,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX) + si;
       if (!mbar_wait(bar, phase, p.err)) break;   // (flagged; the result is lost)
       __syncwarp();
-      const uint4 hd = lds128(wk.aux + si * C::AUX + C::AUX_HEAD);
+      const uint2 hd = lds64(wk.aux + si * C::AUX + C::AUX_HEAD);
       if ((int)hd.x != seg) {
         if (began) wk.write_out(seg);
         else {
