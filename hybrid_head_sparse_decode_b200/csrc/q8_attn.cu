@@ -85,19 +85,11 @@ __device__ __forceinline__ float lds_f(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds_u(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts_u(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -1027,15 +1019,20 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
 constexpr int kMergeThreads = 256;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
+__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8AttnParams p, int beside) {
   constexpr int LPS = D / 4;                 // lanes a state
   constexpr int kGroups = kMergeThreads / LPS;
   __shared__ float s_acc[kGroups][D], s_m[kGroups], s_l[kGroups];
   pdl_launch_dependents();
-  pdl_wait();
+  // Behind a selection (beside) the launch itself came after the attention kernel
+  // had completed; the selection only has to be complete before this kernel is.
+  if (!beside) pdl_wait();
   const int first = blockIdx.x, h = blockIdx.y, ctas = gridDim.x, G = gridDim.y;
   const int seg = p.part_seg[2 * first + 1];
-  if (seg < 0) return;
+  if (seg < 0) {
+    if (beside) pdl_wait();
+    return;
+  }
   int more = 0;
   for (int i0 = first + 1; i0 < ctas; i0 += kMergeThreads) {
     const int i = i0 + threadIdx.x;
@@ -1072,9 +1069,18 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     const int b = seg / p.Hkv, g = seg - b * p.Hkv;
     store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + threadIdx.x, t.l > 0.f ? t.a / t.l : 0.f);
   }
+  if (beside) pdl_wait();
 }
 
-// ---- launches ----------------------------------------------------------------------------------
+// ---- launches ----
+int attn_grid(int sms) { return std::min(sms, kQ8MaxCtas); }
+// A segment per CTA when that leaves no segment over and none is longer than
+// kQ8WholeMax positions: nothing is left open, and one launch less than splitting.
+bool takes_whole(const Q8AttnParams& p, int grid) {
+  return (long long)p.B * p.Hkv <= grid && p.N_max <= kQ8WholeMax;
+}
+
+// ----------------------------------------------------------------------------------
 template <typename T, int CODE, int D, int G, bool HYB>
 cudaError_t launch_g(const Q8AttnParams& p, int grid, cudaStream_t st) {
   using C = Cfg<T, CODE, D, G>;
@@ -1082,8 +1088,7 @@ cudaError_t launch_g(const Q8AttnParams& p, int grid, cudaStream_t st) {
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.run([&] { return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM); });
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(kfn, dim3(grid), dim3(kThreads), C::SMEM, st, p)) != cudaSuccess || p.whole) return e;
-  return launch_pdl(q8_merge_kernel<T, D>, dim3(grid, G), dim3(kMergeThreads), 0, st, p);
+  return launch_pdl(kfn, dim3(grid), dim3(kThreads), C::SMEM, st, p);
 }
 
 template <typename T, int CODE, int D, bool HYB>
@@ -1109,12 +1114,26 @@ cudaError_t launch_c(const Q8AttnParams& p, int D, int grid, cudaStream_t st) {
 
 }  // namespace
 
+cudaError_t launch_q8_merge(const Q8AttnParams& p, int dtype, int D, int sms, bool beside, cudaStream_t st) {
+  const int grid = attn_grid(sms);
+  if (takes_whole(p, grid)) return cudaSuccess;
+  const dim3 g(grid, p.Hq / p.Hkv), b(kMergeThreads);
+  const int w = beside ? 1 : 0;
+  cudaError_t e;
+  if (dtype == 0)
+    e = D == 128 ? launch_pdl(q8_merge_kernel<__nv_bfloat16, 128>, g, b, 0, st, p, w)
+                 : launch_pdl(q8_merge_kernel<__nv_bfloat16, 64>, g, b, 0, st, p, w);
+  else
+    e = D == 128 ? launch_pdl(q8_merge_kernel<float, 128>, g, b, 0, st, p, w)
+                 : launch_pdl(q8_merge_kernel<float, 64>, g, b, 0, st, p, w);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
 cudaError_t launch_q8_attn(const Q8AttnParams& in, int dtype, int code, int D, int sms, cudaStream_t st) {
-  const int grid = std::min(sms, kQ8MaxCtas);
+  const int grid = attn_grid(sms);
   Q8AttnParams p = in;
-  // A segment per CTA when that leaves no segment over and none is longer than
-  // kQ8WholeMax positions: one launch less than splitting.
-  p.whole = (long long)p.B * p.Hkv <= grid && p.N_max <= kQ8WholeMax;
+  p.whole = takes_whole(in, grid);
   cudaError_t e;
   if (dtype == 0)
     e = code == kCodeE4M3 ? launch_c<__nv_bfloat16, kCodeE4M3>(p, D, grid, st)

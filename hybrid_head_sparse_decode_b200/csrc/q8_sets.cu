@@ -8,13 +8,13 @@
 // applied here, once), each with the heads that use it.
 //
 // One CTA a tile.  A set's entries ascend, so the tile's are found by a search with
-// kFan samples a round (39321 entries: three rounds), then set as bits in shared
+// kFan samples a round (39321 entries: two rounds), then set as bits in shared
 // memory; the union's words are counted, prefix-summed and expanded.  Every word and
 // list entry has one writer.  Further CTAs hand the index rows on (a sparse head's
 // set goes on as it came) and check them: an entry out of [0, n_b), not above its
 // predecessor or behind the set's end is flagged.  A row that is not a set may be
 // missed in part by the search; every access stays in bounds.  Bound by latency:
-// three dependent loads, and twice the index rows' bytes.
+// dependent loads, and twice the index rows' bytes.
 #include <algorithm>
 
 #include "q8.cuh"
@@ -26,25 +26,28 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kWords = kQ8Tile / 32;          // words of a tile's bits
-constexpr int kFan = 64;                      // samples a search takes at once (two warps)
-constexpr int kSearches = kThreads / kFan;
-constexpr int kCopyRow = 4 * kThreads;        // entries a copying CTA takes
-constexpr int kMaxG = 8;
+constexpr int kSamples = 4;                   // samples a thread takes in a search
+constexpr int kFan = 64 * kSamples;           // ... and a search (two warps) at once
+constexpr int kSearches = kThreads / 64;
+constexpr int kCopyRow = 16 * kThreads;       // entries a copying CTA takes
+constexpr int kBatch = 8;                     // consecutive entries a thread takes at once
 
 // One tile.  The set of sparse head t of the group: entries [from, to) of its row
 // lie in the tile.
+template <int G>
 __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
-  __shared__ uint32_t s_bits[kMaxG][kWords];
-  __shared__ int s_lo[2 * kMaxG], s_hi[2 * kMaxG], s_n[kWarps];
+  __shared__ uint32_t s_bits[G][kWords];
+  __shared__ int s_lo[2 * G], s_hi[2 * G], s_n[kWarps];
   __shared__ int s_sum[kWarps];
-  __shared__ uint32_t s_rows[kQ8Tile];
+  __shared__ uint16_t s_off[kQ8Tile];
   __shared__ uint8_t s_heads[kQ8Tile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seg = item / p.ntiles, tile = item - seg * p.ntiles;
-  const int b = seg / p.Hkv, g = seg - b * p.Hkv, G = p.Hq / p.Hkv;
+  const int b = seg / p.Hkv, g = seg - b * p.Hkv;
   const int n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
   const int base = tile * kQ8Tile, rows = min(max(n - base, 0), kQ8Tile);
   uint32_t sparse = 0;                        // bit t: head t of the group is sparse
+#pragma unroll
   for (int t = 0; t < G; ++t) {
     const int h = g * G + t;
     if (!((p.role[h >> 5] >> (h & 31)) & 1u)) sparse |= 1u << t;
@@ -57,7 +60,7 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
   }
   const int32_t* row0 = p.idx_in + ((size_t)b * p.Hq + g * G) * p.k;
   for (int i = tid; i < G * kWords; i += kThreads) (&s_bits[0][0])[i] = 0u;
-  if (tid < 2 * kMaxG) {
+  if (tid < 2 * G) {
     s_lo[tid] = 0;
     s_hi[tid] = p.k;
   }
@@ -65,23 +68,28 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
   // search 2t + e: the first entry of head t's row at or above the tile's begin (e =
   // 0) or end; as unsigned numbers the padding's -1 lies above every position
   for (int s0 = 0; s0 < 2 * G; s0 += kSearches) {
-    const int s = s0 + tid / kFan, j = tid % kFan;
+    const int s = s0 + tid / 64, j = tid % 64;
     const bool live = s < 2 * G && ((sparse >> (s >> 1)) & 1u);
     const uint32_t target = (uint32_t)(base + (s & 1) * kQ8Tile);
     const int32_t* row = row0 + (size_t)(s >> 1) * p.k;
     for (int width = p.k; width > 0;) {
       // the answer lies in [lo, hi]: step entries to a sample, the last of each step
       const int step = (width + kFan - 1) / kFan;
-      int lo = 0, hi = 0;
-      bool below = false;
+      int lo = 0, hi = 0, below = 0;
       if (live) {
         lo = s_lo[s];
         hi = s_hi[s];
-        const int at = lo + (j + 1) * step - 1;
-        below = at < hi && (uint32_t)__ldg(&row[at]) < target;
+        uint32_t v[kSamples];
+#pragma unroll
+        for (int i = 0; i < kSamples; ++i) {
+          const int at = lo + (64 * i + j + 1) * step - 1;
+          v[i] = at < hi ? (uint32_t)__ldg(&row[at]) : 0xffffffffu;
+        }
+#pragma unroll
+        for (int i = 0; i < kSamples; ++i) below += v[i] < target;
       }
-      const uint32_t m = __ballot_sync(kFull, below);
-      if (lane == 0) s_n[warp] = __popc(m);
+      below = __reduce_add_sync(kFull, below);
+      if (lane == 0) s_n[warp] = below;
       __syncthreads();
       if (live && j == 0) {
         // (entries ascend: the samples below the target are the first ones)
@@ -98,9 +106,22 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
   if ((sparse >> t) & 1u) {
     const int32_t* row = row0 + (size_t)t * p.k;
     const int to = s_lo[2 * t + 1];
-    for (int e = s_lo[2 * t] + tid % per; e < to; e += per) {
-      const int at = __ldg(&row[e]) - base;
-      if ((unsigned)at < (unsigned)rows) atomicOr(&s_bits[t][at >> 5], 1u << (at & 31));
+    for (int e0 = s_lo[2 * t] + kBatch * (tid % per); e0 < to; e0 += kBatch * per) {
+      int at[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) at[i] = e0 + i < to ? __ldg(&row[e0 + i]) - base : -1;
+      // neighbours share a word: collect them before the atomic
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const bool in = (unsigned)at[i] < (unsigned)rows;
+        if (in) m |= 1u << (at[i] & 31);
+        const bool goes_on = in && i + 1 < kBatch && at[(i + 1) % kBatch] >> 5 == at[i] >> 5;
+        if (in && !goes_on) {
+          atomicOr(&s_bits[t][at[i] >> 5], m);
+          m = 0;
+        }
+      }
     }
   }
   __syncthreads();
@@ -114,10 +135,10 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
   }
   // the union, eight positions a thread
   static_assert(kQ8Tile == 8 * kThreads, "a byte of the bits a thread");
-  uint32_t bits[kMaxG], u = 0;
+  uint32_t bits[G], u = 0;
 #pragma unroll
-  for (int h = 0; h < kMaxG; ++h) {
-    bits[h] = h < G ? (s_bits[h][tid >> 2] >> (8 * (tid & 3))) & 255u : 0u;
+  for (int h = 0; h < G; ++h) {
+    bits[h] = (s_bits[h][tid >> 2] >> (8 * (tid & 3))) & 255u;
     u |= bits[h];
   }
   const int mine = __popc(u);
@@ -135,30 +156,27 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
     if (w < warp) at += s_sum[w];
     total += s_sum[w];
   }
-  if (u) {
-    const int pos = base + 8 * tid;
-    const int page = __ldg(&p.c.table[(size_t)b * p.c.max_pages + (pos >> p.c.page_log2)]);
-    const bool ok = page >= 0 && page < p.c.num_pages;
-    if (!ok) flag_error(p.err, kErrBadIndex);
-    const uint32_t row = ((uint32_t)(page * p.Hkv + g) << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1));
+  for (; u; u &= u - 1) {
+    const int i = __ffs(u) - 1;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((u >> i) & 1u) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int h = 0; h < kMaxG; ++h) m |= ((bits[h] >> i) & 1u) << h;
-        s_rows[at] = ok ? row + i : 0xffffffffu;   // (absent: no head uses it)
-        s_heads[at] = (uint8_t)(ok ? m : 0u);
-        ++at;
-      }
-    }
+    for (int h = 0; h < G; ++h) m |= ((bits[h] >> i) & 1u) << h;
+    s_off[at] = (uint16_t)(8 * tid + i);
+    s_heads[at] = (uint8_t)m;
+    ++at;
   }
   __syncthreads();
   uint32_t* lr = p.list_rows + (size_t)item * kQ8Tile;
   uint8_t* lh = p.list_heads + (size_t)item * kQ8Tile;
+  const int32_t* table = p.c.table + (size_t)b * p.c.max_pages;
+#pragma unroll 4
   for (int i = tid; i < total; i += kThreads) {
-    lr[i] = s_rows[i];
-    lh[i] = s_heads[i];
+    const int pos = base + s_off[i], page = __ldg(&table[pos >> p.c.page_log2]);
+    const bool ok = page >= 0 && page < p.c.num_pages;
+    if (!ok) flag_error(p.err, kErrBadIndex);
+    // (no page: an absent row that no head uses)
+    lr[i] = ok ? ((uint32_t)(page * p.Hkv + g) << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1)) : 0xffffffffu;
+    lh[i] = ok ? s_heads[i] : 0;
   }
   if (tid == 0) p.tile_rows[item] = total;
 }
@@ -177,20 +195,33 @@ __device__ __forceinline__ void hand_on(const Q8AttnParams& p, int item, int par
   const int n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
   const size_t row = ((size_t)b * p.Hq + s_head[pair - b * p.n_sparse]) * p.k;
   const int32_t* in = p.idx_in + row;
+  constexpr int N = 8;
+  const int lane = threadIdx.x & 31;
   bool bad = false;
+  const int end = min(p.k, (part + 1) * kCopyRow);
+  for (int e0 = part * kCopyRow; e0 < end; e0 += N * kThreads) {
+    int v[N], before[N];          // lane 0 also reads the entry before its own
 #pragma unroll
-  for (int i = 0; i < kCopyRow / kThreads; ++i) {
-    const int e = part * kCopyRow + i * kThreads + threadIdx.x;
-    if (e < p.k) {
-      const int v = __ldg(&in[e]), prev = e > 0 ? __ldg(&in[e - 1]) : -1;
-      if (v >= 0) bad = bad || v >= n || (e > 0 && (prev < 0 || v <= prev));
-      p.idx_out[row + e] = v;
+    for (int i = 0; i < N; ++i) {
+      const int e = e0 + i * kThreads + threadIdx.x;
+      v[i] = e < end ? __ldg(&in[e]) : -1;
+      before[i] = lane == 0 && e > 0 && e < end ? __ldg(&in[e - 1]) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = e0 + i * kThreads + threadIdx.x;
+      const int up = __shfl_up_sync(kFull, v[i], 1), prev = lane == 0 ? before[i] : up;
+      if (e < end) {
+        if (v[i] >= 0) bad = bad || v[i] >= n || (e > 0 && (prev < 0 || v[i] <= prev));
+        p.idx_out[row + e] = v[i];
+      }
     }
   }
   if (bad) flag_error(p.err, kErrBadIndex);
 }
 
-__global__ void __launch_bounds__(kThreads) q8_sets_kernel(const __grid_constant__ Q8AttnParams p, int tiles, int parts,
+template <int G>
+__global__ void __launch_bounds__(kThreads, 3) q8_sets_kernel(const __grid_constant__ Q8AttnParams p, int tiles, int parts,
                                                            int out_words) {
   pdl_launch_dependents();
   pdl_wait();
@@ -198,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) q8_sets_kernel(const __grid_constant
   for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < (long long)p.B * p.Hq * out_words;
        i += (long long)gridDim.x * kThreads)
     out[i] = 0u;
-  if ((int)blockIdx.x < tiles) build_tile(p, blockIdx.x);
+  if ((int)blockIdx.x < tiles) build_tile<G>(p, blockIdx.x);
   else hand_on(p, (int)blockIdx.x - tiles, parts);
 }
 
@@ -210,7 +241,16 @@ cudaError_t launch_q8_sets(const Q8AttnParams& p, int dtype, int D, cudaStream_t
   const long long grid = tiles + (long long)p.B * p.n_sparse * parts;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int out_words = D * (dtype == 0 ? 2 : 4) / 4;
-  const cudaError_t e = launch_pdl(q8_sets_kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, p, (int)tiles, parts, out_words);
+  auto launch = [&](auto kfn) {
+    return launch_pdl(kfn, dim3((unsigned)grid), dim3(kThreads), 0, st, p, (int)tiles, parts, out_words);
+  };
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (p.Hq / p.Hkv) {
+    case 1: e = launch(q8_sets_kernel<1>); break;
+    case 2: e = launch(q8_sets_kernel<2>); break;
+    case 4: e = launch(q8_sets_kernel<4>); break;
+    case 8: e = launch(q8_sets_kernel<8>); break;
+  }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

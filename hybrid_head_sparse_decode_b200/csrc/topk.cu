@@ -340,13 +340,14 @@ __global__ void __launch_bounds__(kThreads, D >= 128 ? 2 : 1)
     topk_combine_kernel(const __grid_constant__ TopkParams p, const __grid_constant__ CombineParams cp,
                         int keys_cap, int wpc_cap, int ntopk, int ncomb) {
   extern __shared__ __align__(16) uint32_t dsm[];
-  pdl_launch_dependents();
+  if (!p.trigger_late) pdl_launch_dependents();
   static_assert(C % kCombineSplit == 0, "a head's combine CTAs share a cluster");
   const int cta = blockIdx.x;
   unsigned char* csm = reinterpret_cast<unsigned char*>(dsm);
   if (cta < ntopk) topk_prologue<C>(dsm);
   else combine_prologue<D>(csm);
   pdl_wait();
+  if (p.trigger_late) pdl_launch_dependents();
   if (cta < ntopk) topk_body<C>(p, keys_cap, wpc_cap, cta, dsm);
   else if (cta - ntopk < ncomb) combine_body<T, D>(cp, cta - ntopk, csm);
   else combine_idle();
@@ -478,7 +479,7 @@ cudaError_t launch_tc_d(const TopkParams& p, const CombineParams& cp, cudaStream
   // beside the next layer's attention kernel, and a cluster of 8 needs 4 free
   // SMs at once where one of 16 needs 8 (measured: the 36-layer 128K step is
   // about 50 us shorter).
-  if (cp.B == 0) return launch_tc<8, T, D>(p, cp, st);
+  if (cp.B == 0 && !p.alone) return launch_tc<8, T, D>(p, cp, st);
   const long long ctas16 = 16LL * p.B * p.nheads;
   const bool one_wave = p.sms <= 0 || ctas16 <= 2LL * p.sms;
   const bool long_rows = p.N_max > 32768;
