@@ -79,6 +79,8 @@ _lib = None
 def load(path: str | None = None):
     """Load liblychee.so (built in-tree by hybrid_head_sparse_decode_b200.build)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

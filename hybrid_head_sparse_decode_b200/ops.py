@@ -336,56 +336,105 @@ def alloc_q8_workspace(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev):
-    """The checked cache of a call: its shape and pointers for the library."""
-    if not isinstance(cache, Q8Cache):
-        raise TypeError("cache must be a Q8Cache")
-    _need_cuda("cache.k", cache.k, device=dev)
-    if cache.k.dtype not in _CODE:
-        raise TypeError(f"cache.k must be torch.float8_e4m3fn or torch.int8, got {cache.k.dtype}")
-    if cache.k.dim() != 4 or cache.k.shape[3] != d:
-        raise ValueError(f"cache.k must be [num_pages, Hkv, page, {d}], got {tuple(cache.k.shape)}")
-    P, Hkv, page, _ = cache.k.shape
-    _need_cuda("cache.v", cache.v, cache.k.dtype, (P, Hkv, page, d), device=dev)
-    _need_cuda("cache.k_scale", cache.k_scale, torch.float32, (P, Hkv), device=dev)
-    _need_cuda("cache.v_scale", cache.v_scale, torch.float32, (P, Hkv), device=dev)
-    _need_cuda("block_table", block_table, torch.int32, device=dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, max_pages = block_table.shape
-    _need_cuda("seqlens", seqlens, torch.int32, (B,), device=dev)
-    sh = make_q8_shape(B, Hq, Hkv, d, page, P, max_pages, dt, cache.k.dtype)
-    ptrs = N.Q8CachePtrs(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-                         cache.v_scale.data_ptr(), block_table.data_ptr())
-    return sh, ptrs
+# The calls below run once a layer and token, so what they do on the host counts: a
+# tensor that is as it must be passes one short test, and only another one goes
+# through the checks that name what is wrong.
+
+def _need(name, t, dtype, shape, dev, index):
+    """_need_cuda, quick where there is nothing to report."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == index and t.is_contiguous()):
+        _need_cuda(name, t, dtype, shape, device=dev)
 
 
-def _need_rows(name, t, dt, shape, dev):
-    """Rows [T, heads, d] of dtype dt whose tokens may lie further apart than a row's end (a part
-    of a projection's output).  Returns the elements from one token to the next."""
+def _device_index(name, t):
+    """The index of a CUDA tensor's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (there is no CPU path)")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, but the call runs on {dev}")
-    if t.dtype != dt:
+    return t.get_device()
+
+
+# The current stream of a device as a raw handle (without the Stream object where torch has a call for it).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _q8_launch(what, fn, dev, index, stream, args):
+    """Call the library on device `index` with the raw stream as the last argument."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, but the call runs on {dev}")
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
+    if st != N.OK:
+        raise N.LycheeError(st, what)
+
+
+def _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev, index):
+    """The checked cache of a call: its shape and pointers for the library."""
+    if not isinstance(cache, Q8Cache):
+        raise TypeError("cache must be a Q8Cache")
+    k, v, ks, vs = cache
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("cache.k must be a torch.Tensor")
+    code = _CODE.get(k.dtype)
+    if code is None:
+        raise TypeError(f"cache.k must be torch.float8_e4m3fn or torch.int8, got {k.dtype}")
+    shape = k.shape
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"cache.k must be [num_pages, Hkv, page, {d}], got {tuple(shape)}")
+    P, Hkv, page, _ = shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [B, max_pages]")
+    B, max_pages = block_table.shape
+    try:
+        fine = (k.get_device() == index and v.get_device() == index and ks.get_device() == index and
+                vs.get_device() == index and block_table.get_device() == index and
+                seqlens.get_device() == index and v.dtype is k.dtype and ks.dtype is torch.float32 and
+                vs.dtype is torch.float32 and block_table.dtype is torch.int32 and
+                seqlens.dtype is torch.int32 and v.shape == shape and ks.shape == (P, Hkv) and
+                vs.shape == (P, Hkv) and seqlens.shape == (B,) and k.is_contiguous() and
+                v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous() and
+                block_table.is_contiguous() and seqlens.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _need_cuda("cache.k", k, device=dev)
+        _need_cuda("cache.v", v, k.dtype, shape, device=dev)
+        _need_cuda("cache.k_scale", ks, torch.float32, (P, Hkv), device=dev)
+        _need_cuda("cache.v_scale", vs, torch.float32, (P, Hkv), device=dev)
+        _need_cuda("block_table", block_table, torch.int32, device=dev)
+        _need_cuda("seqlens", seqlens, torch.int32, (B,), device=dev)
+    return (N.Q8Shape(B, Hq, Hkv, d, page, P, max_pages, _DT[dt], code),
+            N.Q8CachePtrs(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                          block_table.data_ptr()), B, Hkv)
+
+
+def _need_rows(name, t, dt, shape, dev, index):
+    """Rows [T, heads, d] of dtype dt whose tokens may lie further apart than a row's end (a part
+    of a projection's output).  Returns the elements from one token to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index:
+        _need_cuda(name, t, device=dev)
+    if t.dtype is not dt:
         raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     T, heads, d = shape
-    ok = t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)
-    stride = t.stride(0) if T > 1 else heads * d
-    if not ok or stride < heads * d:
+    s0, s1, s2 = t.stride()
+    if T <= 1:
+        s0 = heads * d
+    if s2 != 1 or (heads > 1 and s1 != d) or s0 < heads * d:
         raise ValueError(f"{name}: the rows of one token must be contiguous")
-    if stride * t.element_size() % 16 != 0 or t.data_ptr() % 16 != 0:
+    if s0 * (2 if dt is torch.bfloat16 else 4) % 16 != 0 or t.data_ptr() % 16 != 0:
         raise ValueError(f"{name}: tokens must begin on 16-byte boundaries")
-    return stride
-
-
-def _need_error(device_error, dev):
-    if device_error is not None:
-        _need_cuda("device_error", device_error, torch.int32, (1,), device=dev)
+    return s0
 
 
 def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q=None, cu_new=None,
@@ -397,94 +446,98 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
     seqlens [B] int32 counts the new tokens.  cos_sin [n_pos, rot] fp32: cosines, then sines, of
     every position's rot / 2 angles (None: no rotation); interleaved: pairs (2i, 2i + 1) instead of
     (i, i + rot / 2).  Rows of k_new, v_new and q may be parts of one projection output.
-    Returns the rotated queries [T, Hq, d], or None without q."""
+    device_error [1] int32 (or None): error bits are OR-ed into it (1 bad page, 2 bad length, 16 a
+    value that is not finite).  Returns the rotated queries [T, Hq, d], or None without q."""
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be a tensor [T, Hkv, d]")
-    T, Hkv, d = k_new.shape
-    dt, dev = k_new.dtype, k_new.device
+    shape, dt, dev = k_new.shape, k_new.dtype, k_new.device
+    T, Hkv, d = shape
     if dt not in _DT:
         raise TypeError(f"k_new must be torch.bfloat16 or torch.float32, got {dt}")
-    ks = _need_rows("k_new", k_new, dt, (T, Hkv, d), dev)
-    vs = _need_rows("v_new", v_new, dt, (T, Hkv, d), dev)
-    Hq, qs = Hkv, 0
+    index = _device_index("k_new", k_new)
+    tok = N.Q8Tokens()
+    tok.k_stride = _need_rows("k_new", k_new, dt, shape, dev, index)
+    tok.v_stride = _need_rows("v_new", v_new, dt, shape, dev, index)
+    tok.k, tok.v, tok.T = k_new.data_ptr(), v_new.data_ptr(), T
+    Hq = Hkv
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be a tensor [T, Hq, d]")
         Hq = q.shape[1]
-        qs = _need_rows("q", q, dt, (T, Hq, d), dev)
+        tok.q_stride = _need_rows("q", q, dt, (T, Hq, d), dev, index)
         if q_out is None:
             q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
-        _need_cuda("q_out", q_out, dt, (T, Hq, d), device=dev)
+        else:
+            _need("q_out", q_out, dt, (T, Hq, d), dev, index)
+        tok.q, tok.q_out = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    sh, ptrs = _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev)
-    if cache.k.shape[1] != Hkv:
-        raise ValueError(f"k_new has {Hkv} heads, the cache {cache.k.shape[1]}")
+    sh, ptrs, B, cache_heads = _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev, index)
+    if cache_heads != Hkv:
+        raise ValueError(f"k_new has {Hkv} heads, the cache {cache_heads}")
     if cu_new is not None:
-        _need_cuda("cu_new", cu_new, torch.int32, (sh.B + 1,), device=dev)
-    elif T != sh.B:
-        raise ValueError(f"without cu_new there is one token a sequence: got {T} for {sh.B}")
-    n_pos = rot = 0
+        _need("cu_new", cu_new, torch.int32, (B + 1,), dev, index)
+        tok.cu_new = cu_new.data_ptr()
+    elif T != B:
+        raise ValueError(f"without cu_new there is one token a sequence: got {T} for {B}")
     if cos_sin is not None:
-        _need_cuda("cos_sin", cos_sin, torch.float32, device=dev)
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [n_pos, rot]")
-        n_pos, rot = cos_sin.shape
-    _need_error(device_error, dev)
-    if T == 0:
-        return q_out
-    tok = N.Q8Tokens(k_new.data_ptr(), v_new.data_ptr(), None if q is None else q.data_ptr(),
-                     None if q is None else q_out.data_ptr(), ks, vs, qs,
-                     None if cos_sin is None else cos_sin.data_ptr(),
-                     None if cu_new is None else cu_new.data_ptr(), T, n_pos, rot,
-                     int(bool(interleaved)))
-    with torch.cuda.device(dev):
-        st = N.load().lychee_append_rope_q8(ctypes.byref(sh), ctypes.byref(ptrs), ctypes.byref(tok),
-                                            _ptr(seqlens), _ptr(device_error),
-                                            _stream_handle(stream, dev))
-    _check(st, "lychee_append_rope_q8")
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a tensor [n_pos, rot]")
+        _need("cos_sin", cos_sin, torch.float32, cos_sin.shape, dev, index)
+        tok.n_pos, tok.rot = cos_sin.shape
+        tok.cos_sin = cos_sin.data_ptr()
+    tok.interleaved = 1 if interleaved else 0
+    err = None
+    if device_error is not None:
+        _need("device_error", device_error, torch.int32, (1,), dev, index)
+        err = device_error.data_ptr()
+    if T > 0:
+        _q8_launch("lychee_append_rope_q8", N.load().lychee_append_rope_q8, dev, index, stream,
+                   (sh, ptrs, tok, seqlens.data_ptr(), err))
     return q_out
 
 
-def _q8_query(q, out):
-    _need_cuda("q", q)
+def _q8_call(q, cache, block_table, seqlens, out, workspace, device_error, k):
+    """What both attention calls check and make: (shape, pointers, B, Hq, device, its index, out,
+    workspace, device_error's pointer)."""
+    index = _device_index("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, d]")
-    if q.dtype not in _DT:
-        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {q.dtype}")
+    shape, dt, dev = q.shape, q.dtype, q.device
+    if dt not in _DT:
+        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
+    _need("q", q, dt, shape, dev, index)
     if out is None:
         out = torch.empty_like(q)
-    _need_cuda("out", out, q.dtype, tuple(q.shape), device=q.device)
-    return out
-
-
-def _q8_workspace(workspace, sh, k, dev):
+    else:
+        _need("out", out, dt, shape, dev, index)
+    sh, ptrs, B, _ = _q8_cache(cache, block_table, seqlens, shape[1], shape[2], dt, dev, index)
+    if B != shape[0]:
+        raise ValueError(f"q has {shape[0]} sequences, block_table {B}")
     if workspace is None:
-        n = N.load().lychee_q8_workspace_size(ctypes.byref(sh), int(k))
+        n = N.load().lychee_q8_workspace_size(sh, k)
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    _need_cuda("workspace", workspace, torch.uint8, device=dev)
-    return workspace
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
+              workspace.get_device() == index and workspace.is_contiguous()):
+        _need_cuda("workspace", workspace, torch.uint8, device=dev)
+    err = None
+    if device_error is not None:
+        _need("device_error", device_error, torch.int32, (1,), dev, index)
+        err = device_error.data_ptr()
+    return sh, ptrs, B, shape[1], dev, index, out, workspace, err
 
 
 def decode_attn_q8(q, cache, block_table, seqlens, *, out=None, workspace=None, device_error=None,
                    stream=None):
     """Attention of one query token a sequence over every position of the 8-bit paged cache.
     q [B, Hq, d] (bf16 or fp32), block_table [B, max_pages] int32, seqlens [B] int32.
-    Returns out [B, Hq, d]."""
-    out = _q8_query(q, out)
-    B, Hq, d = q.shape
-    dev = q.device
-    sh, ptrs = _q8_cache(cache, block_table, seqlens, Hq, d, q.dtype, dev)
-    if sh.B != B:
-        raise ValueError(f"q has {B} sequences, block_table {sh.B}")
-    _need_error(device_error, dev)
-    workspace = _q8_workspace(workspace, sh, 0, dev)
-    with torch.cuda.device(dev):
-        st = N.load().lychee_decode_attn_q8(ctypes.byref(sh), _ptr(q), ctypes.byref(ptrs),
-                                            _ptr(seqlens), _ptr(out), _ptr(workspace),
-                                            ctypes.c_size_t(workspace.numel()), _ptr(device_error),
-                                            _stream_handle(stream, dev))
-    _check(st, "lychee_decode_attn_q8")
+    workspace: uint8, q8_workspace_size(...) bytes (calls that share one must be ordered on one
+    stream; None: a fresh one).  device_error as in append_rope_q8.  Returns out [B, Hq, d]."""
+    sh, ptrs, _, _, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,
+                                                               workspace, device_error, 0)
+    _q8_launch("lychee_decode_attn_q8", N.load().lychee_decode_attn_q8, dev, index, stream,
+               (sh, q.data_ptr(), ptrs, seqlens.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                workspace.numel(), err))
     return out
 
 
@@ -492,31 +545,31 @@ def hybrid_decode_attn_q8(q, cache, block_table, seqlens, head_role, idx_in, k, 
                           out=None, idx_out=None, workspace=None, device_error=None, stream=None,
                           block=0):
     """hybrid_decode_attn over the 8-bit paged cache: one hybrid-head layer.  q, head_role, idx_in,
-    k, k_per_seq and block as there; cache, block_table and seqlens as in decode_attn_q8.
+    k, k_per_seq and block as there; cache, block_table, seqlens, workspace (q8_workspace_size(...,
+    k) bytes) and device_error as in decode_attn_q8.
     Returns (out [B, Hq, d], idx_out [B, Hq, k])."""
-    out = _q8_query(q, out)
-    B, Hq, d = q.shape
-    dev = q.device
-    sh, ptrs = _q8_cache(cache, block_table, seqlens, Hq, d, q.dtype, dev)
-    if sh.B != B:
-        raise ValueError(f"q has {B} sequences, block_table {sh.B}")
+    k = int(k)
+    sh, ptrs, B, Hq, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,
+                                                                workspace, device_error, max(k, 0))
+    kps = idx = None
     if k_per_seq is not None:
-        _need_cuda("k_per_seq", k_per_seq, torch.int32, (B,), device=dev)
+        _need("k_per_seq", k_per_seq, torch.int32, (B,), dev, index)
+        kps = k_per_seq.data_ptr()
     if idx_in is not None:
-        _need_cuda("idx_in", idx_in, torch.int32, (B, Hq, k), device=dev)
-    role = _roles_host(head_role, Hq)
+        _need("idx_in", idx_in, torch.int32, (B, Hq, k), dev, index)
+        idx = idx_in.data_ptr()
+    role = head_role
+    if not (isinstance(role, torch.Tensor) and role.dtype is torch.uint8 and role.shape == (Hq,) and
+            not role.is_cuda and role.is_contiguous()):
+        role = _roles_host(head_role, Hq)
     if idx_out is None:
-        idx_out = torch.empty((B, Hq, k), dtype=torch.int32, device=dev)
-    _need_cuda("idx_out", idx_out, torch.int32, (B, Hq, k), device=dev)
-    _need_error(device_error, dev)
-    workspace = _q8_workspace(workspace, sh, k, dev)
-    with torch.cuda.device(dev):
-        st = N.load().lychee_hybrid_decode_attn_q8(
-            ctypes.byref(sh), ctypes.c_int32(int(k)), ctypes.c_int32(int(block)), _ptr(q),
-            ctypes.byref(ptrs), _ptr(seqlens), _ptr(k_per_seq), ctypes.c_void_p(role.data_ptr()),
-            _ptr(idx_in), _ptr(out), _ptr(idx_out), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel()), _ptr(device_error), _stream_handle(stream, dev))
-    _check(st, "lychee_hybrid_decode_attn_q8")
+        idx_out = torch.empty((B, Hq, max(k, 0)), dtype=torch.int32, device=dev)
+    else:
+        _need("idx_out", idx_out, torch.int32, (B, Hq, k), dev, index)
+    _q8_launch("lychee_hybrid_decode_attn_q8", N.load().lychee_hybrid_decode_attn_q8, dev, index,
+               stream, (sh, k, int(block), q.data_ptr(), ptrs, seqlens.data_ptr(), kps,
+                        role.data_ptr(), idx, out.data_ptr(), idx_out.data_ptr(),
+                        workspace.data_ptr(), workspace.numel(), err))
     return out, idx_out
 
 
