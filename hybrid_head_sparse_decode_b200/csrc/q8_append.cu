@@ -14,8 +14,14 @@
 // Work split.  Every scale has one writer: a CTA takes one (page, head, K or V),
 // reads its new rows once into registers, reduces the magnitude and writes codes
 // and scale.  No atomics, so results do not depend on scheduling.  Further CTAs
-// rotate the queries.  A row is shared by D / 8 lanes of eight elements each.
-// It is bound by memory for prompts and by latency for single tokens.
+// rotate the queries, a warp taking one token's heads (or a part of them while
+// there are few tokens), so that the angles are read once for many heads.  A lane
+// takes W dimensions and the W that pair with them, 16 bytes each: 8 of bf16, 4 of
+// fp32 (and of bf16 when rot is an odd multiple of 8).  Rows wait as they lie in
+// memory and are turned twice, for the magnitude and for the codes: that costs less
+// than the registers of their values (64 a thread, 1024 threads an SM).  Bound by
+// memory for prompts (8903 tokens of 32 query and 8 KV heads of 128 in bf16: 44 us,
+// 4.6 TB/s in and out), by latency for single tokens (2.8 us).
 #include <algorithm>
 
 #include "q8.cuh"
@@ -25,64 +31,114 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeadsPerItem = 4;   // query heads a lane group turns with one load of the angles
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&o)[4]);
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&o)[4]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-  o[0] = a.x; o[1] = a.y; o[2] = b.x; o[3] = b.y;
+// W elements as they lie in memory (kept so while they wait: half the registers of
+// their fp32 values), and their values.
+template <typename T, int W>
+struct Raw {
+  static constexpr int N = W * (int)sizeof(T) / 4;   // 2, 4 or 8 words
+  uint32_t w[N];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x; w[1] = x.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&o)[W]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        const float2 a = bf16x2_to_float2(w[i]);
+        o[2 * i] = a.x;
+        o[2 * i + 1] = a.y;
+      } else {
+        o[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+};
+template <int W>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&y)[W]) {
+  uint32_t w[W / 2];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&a);
+  }
+  if constexpr (W == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, float (&o)[4]) {
-  const float4 w = *reinterpret_cast<const float4*>(p);
-  o[0] = w.x; o[1] = w.y; o[2] = w.z; o[3] = w.w;
+template <int W>
+__device__ __forceinline__ void store_row(float* p, const float (&y)[W]) {
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* y) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-__device__ __forceinline__ void store4(float* p, const float* y) {
-  *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+// W values -> W codes at p.
+template <int CODE, int W>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&y)[W], float f) {
+  const uint32_t lo = quantise4<CODE>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+  if constexpr (W == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, quantise4<CODE>(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
+  else *reinterpret_cast<uint32_t*>(p) = lo;
 }
 
-// The eight dimensions of lane j of a row: four at a, four at b, and whether they
-// are four rotated pairs (pairs 4j .. 4j + 3).  Half-split pairs are (i, i + rot /
-// 2); interleaved ones (2i, 2i + 1) lie in eight consecutive dimensions, as do the
-// dimensions past rot (rot is a multiple of 8).
+// The 2 W dimensions of lane j of a row: W at a, W at b, and whether they are W
+// rotated pairs (pairs W j ...).  Half-split pairs are (i, i + rot / 2); interleaved
+// ones (2i, 2i + 1) lie in 2 W consecutive dimensions, as do the dimensions past rot
+// (rot is a multiple of 2 W).
 struct LaneDims {
   int a, b;
-  bool turn, adjacent;
+  bool turn;
 };
+template <int W>
 __device__ __forceinline__ LaneDims lane_dims(int j, int rot, bool interleaved) {
   LaneDims l;
-  l.turn = 8 * j < rot;
-  l.adjacent = interleaved;
-  l.a = l.turn && !interleaved ? 4 * j : 8 * j;
-  l.b = l.turn && !interleaved ? rot / 2 + 4 * j : 8 * j + 4;
+  l.turn = 2 * W * j < rot;
+  l.a = l.turn && !interleaved ? W * j : 2 * W * j;
+  l.b = l.turn && !interleaved ? rot / 2 + W * j : 2 * W * j + W;
   return l;
 }
 
-__device__ __forceinline__ void turn_pairs(float (&x)[4], float (&y)[4], float4 c, float4 s,
-                                           bool adjacent) {
-  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+template <int W>
+__device__ __forceinline__ void load_angles(const Q8AppendParams& p, int pos, int j, float (&c)[W], float (&s)[W]) {
+  const float* at = p.cos_sin + (size_t)pos * p.rot + W * j;
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(at) + i);
+    const float4 y = __ldg(reinterpret_cast<const float4*>(at + p.rot / 2) + i);
+    c[4 * i] = x.x; c[4 * i + 1] = x.y; c[4 * i + 2] = x.z; c[4 * i + 3] = x.w;
+    s[4 * i] = y.x; s[4 * i + 1] = y.y; s[4 * i + 2] = y.z; s[4 * i + 3] = y.w;
+  }
+}
+template <int W>
+__device__ __forceinline__ void turn_pairs(float (&x)[W], float (&y)[W], const float (&c)[W], const float (&s)[W],
+                                           bool interleaved) {
   auto turn = [](float& x1, float& x2, float cv, float sv) {
     const float y1 = __fsub_rn(__fmul_rn(x1, cv), __fmul_rn(x2, sv));
     const float y2 = __fadd_rn(__fmul_rn(x2, cv), __fmul_rn(x1, sv));
     x1 = y1;
     x2 = y2;
   };
-  if (adjacent) {
-    turn(x[0], x[1], cc[0], ss[0]);
-    turn(x[2], x[3], cc[1], ss[1]);
-    turn(y[0], y[1], cc[2], ss[2]);
-    turn(y[2], y[3], cc[3], ss[3]);
+  if (interleaved) {
+#pragma unroll
+    for (int e = 0; e < W / 2; ++e) {
+      turn(x[2 * e], x[2 * e + 1], c[e], s[e]);
+      turn(y[2 * e], y[2 * e + 1], c[W / 2 + e], s[W / 2 + e]);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) turn(x[e], y[e], cc[e], ss[e]);
+    for (int e = 0; e < W; ++e) turn(x[e], y[e], c[e], s[e]);
   }
 }
 
@@ -123,8 +179,29 @@ __device__ __forceinline__ int find_block(const Q8AppendParams& p, int blk, bool
     j = rows.first >> p.c.page_log2;
     return rows.m > 0 ? blk : -1;
   }
-  __shared__ int s_sum[kWarps], s_b, s_j;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (p.B <= 32) {
+    // every warp by itself
+    NewRows r{0, 0, 0};
+    if (lane < p.B) r = new_rows(p, lane, flag && warp == 0);
+    const int first = r.first >> p.c.page_log2;
+    const int nb = r.m > 0 ? ((r.first + r.m - 1) >> p.c.page_log2) - first + 1 : 0;
+    int incl = nb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, blk >= incl - nb && blk < incl);
+    if (!here) return -1;
+    const int l = __ffs(here) - 1;
+    j = __shfl_sync(0xffffffffu, first + blk - (incl - nb), l);
+    rows.t0 = __shfl_sync(0xffffffffu, r.t0, l);
+    rows.m = __shfl_sync(0xffffffffu, r.m, l);
+    rows.first = __shfl_sync(0xffffffffu, r.first, l);
+    return l;
+  }
+  __shared__ int s_sum[kWarps], s_b, s_j;
   if (threadIdx.x == 0) s_b = -1;
   int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -163,9 +240,9 @@ __device__ __forceinline__ int find_block(const Q8AppendParams& p, int blk, bool
 }
 
 // One (block, head, K or V).  ITERS: rows each lane group may hold.
-template <typename T, int CODE, int D, int ITERS>
+template <typename T, int CODE, int D, int W, int ITERS>
 __device__ __forceinline__ void append_block(const Q8AppendParams& p, int item) {
-  constexpr int LPR = D / 8;              // lanes a row
+  constexpr int LPR = D / (2 * W);        // lanes a row
   constexpr int RPI = kThreads / LPR;     // rows at once
   const int units = 2 * p.Hkv;
   const int blk = item / units, u = item % units;
@@ -188,35 +265,42 @@ __device__ __forceinline__ void append_block(const Q8AppendParams& p, int item) 
   const bool goes_on = lo > base;         // the block holds rows of the sequence already
   const float old_scale = goes_on ? *scale : 0.f;
   const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
-  const LaneDims ld = lane_dims(l, is_v || !p.cos_sin ? 0 : p.rot, p.interleaved != 0);
-  const T* src = static_cast<const T*>(is_v ? p.v_new : p.k_new) +
-                 (size_t)(rows.t0 + lo - rows.first) * (is_v ? p.v_stride : p.k_stride) + g * D;
+  const LaneDims ld = lane_dims<W>(l, is_v || !p.cos_sin ? 0 : p.rot, p.interleaved != 0);
   const long long stride = is_v ? p.v_stride : p.k_stride;
-  float xa[ITERS][4], xb[ITERS][4];
+  const T* src = static_cast<const T*>(is_v ? p.v_new : p.k_new) + (size_t)(rows.t0 + lo - rows.first) * stride + g * D;
+  Raw<T, W> ra[ITERS], rb[ITERS];
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const int r = r0 + i * RPI;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) xa[i][e] = xb[i][e] = 0.f;
+    ra[i].clear();
+    rb[i].clear();
     if (lo + r < hi) {
-      load4<T>(src + r * stride + ld.a, xa[i]);
-      load4<T>(src + r * stride + ld.b, xb[i]);
+      ra[i].load(src + r * stride + ld.a);
+      rb[i].load(src + r * stride + ld.b);
     }
   }
+  // the values of row r (turned again for the codes: cheaper than the registers)
+  auto row_values = [&](int i, int r, float (&xa)[W], float (&xb)[W]) {
+    ra[i].values(xa);
+    rb[i].values(xb);
+    if (ld.turn) {
+      float c[W], s[W];
+      load_angles<W>(p, lo + r, l, c, s);
+      turn_pairs<W>(xa, xb, c, s, p.interleaved != 0);
+    }
+  };
   float amax = 0.f;
   bool finite = true;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const int r = r0 + i * RPI;
     if (lo + r < hi) {
-      if (ld.turn) {
-        const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + (size_t)(lo + r) * p.rot + 4 * l);
-        turn_pairs(xa[i], xb[i], __ldg(cs), __ldg(cs + p.rot / 8), ld.adjacent);
-      }
+      float xa[W], xb[W];
+      row_values(i, r, xa, xb);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < W; ++e) {
         // infinities saturate: they do not set the scale
-        const float a = fabsf(xa[i][e]), c = fabsf(xb[i][e]);
+        const float a = fabsf(xa[e]), c = fabsf(xb[e]);
         const bool fa = a < INFINITY, fc = c < INFINITY;
         amax = fmaxf(amax, fmaxf(fa ? a : 0.f, fc ? c : 0.f));
         finite = finite && fa && fc;
@@ -237,11 +321,14 @@ __device__ __forceinline__ void append_block(const Q8AppendParams& p, int item) 
     // the old rows move to the larger scale
     const float ratio = __fdiv_rn(old_scale, now);
     for (int r = r0; r < lo - base; r += RPI) {
-      uint2* at = reinterpret_cast<uint2*>(codes + (size_t)r * D + 8 * l);
-      const uint2 w = *at;
-      const float4 a = codes_to_float<CODE>(w.x), c = codes_to_float<CODE>(w.y);
-      *at = make_uint2(quantise4<CODE>(a.x * ratio, a.y * ratio, a.z * ratio, a.w * ratio),
-                       quantise4<CODE>(c.x * ratio, c.y * ratio, c.z * ratio, c.w * ratio));
+      uint2* at = reinterpret_cast<uint2*>(codes + (size_t)r * D + 2 * W * l);
+#pragma unroll
+      for (int u = 0; u < W / 4; ++u) {
+        const uint2 w = at[u];
+        const float4 a = codes_to_float<CODE>(w.x), c = codes_to_float<CODE>(w.y);
+        at[u] = make_uint2(quantise4<CODE>(a.x * ratio, a.y * ratio, a.z * ratio, a.w * ratio),
+                           quantise4<CODE>(c.x * ratio, c.y * ratio, c.z * ratio, c.w * ratio));
+      }
     }
   }
   // scales are powers of two: multiplying by the reciprocal divides exactly
@@ -251,101 +338,115 @@ __device__ __forceinline__ void append_block(const Q8AppendParams& p, int item) 
     const int r = r0 + i * RPI;
     if (lo + r < hi) {
       uint8_t* dst = codes + (size_t)(lo - base + r) * D;
-      const float (&a)[4] = xa[i], (&c)[4] = xb[i];
-      *reinterpret_cast<uint32_t*>(dst + ld.a) = quantise4<CODE>(
-          a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-      *reinterpret_cast<uint32_t*>(dst + ld.b) = quantise4<CODE>(
-          c[0] * inv, c[1] * inv, c[2] * inv, c[3] * inv);
+      float xa[W], xb[W];
+      row_values(i, r, xa, xb);
+      store_codes<CODE, W>(dst + ld.a, xa, inv);
+      store_codes<CODE, W>(dst + ld.b, xb, inv);
     }
   }
   if (threadIdx.x == 0) *scale = now;
 }
 
-// kHeadsPerItem query heads of one token per lane group.
-template <typename T, int D>
-__device__ __forceinline__ void rotate_q(const Q8AppendParams& p, int cta) {
-  constexpr int LPR = D / 8;
-  constexpr int RPI = kThreads / LPR;
-  const int parts = (p.Hq + kHeadsPerItem - 1) / kHeadsPerItem;
-  const long long item = (long long)cta * RPI + threadIdx.x / LPR;
+// A warp: query heads h0 .. h0 + n of one token, its lane groups side by side.
+template <typename T, int D, int W>
+__device__ __forceinline__ void rotate_q(const Q8AppendParams& p, int cta, int parts) {
+  constexpr int LPR = D / (2 * W);
+  constexpr int RPW = 32 / LPR;          // heads at once
+  constexpr int U = 2;                   // ... and steps in flight (4: fewer warps fit, 52 us against 44)
+  const long long item = (long long)cta * kWarps + (threadIdx.x >> 5);
   if (item >= (long long)p.T * parts) return;
-  const int t = (int)(item / parts), h0 = (int)(item % parts) * kHeadsPerItem;
-  const int l = threadIdx.x % LPR;
+  const int t = (int)(item / parts), part = (int)(item - (long long)t * parts);
+  const int per = (p.Hq + parts - 1) / parts, h_end = min(p.Hq, (part + 1) * per);
+  const int lane = threadIdx.x & 31, l = lane % LPR;
   int b = t;
   if (p.cu_new) {
-    // the last sequence that begins at or before t
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(&p.cu_new[mid]) <= t) lo = mid;
-      else hi = mid;
+    if (p.B <= 32) {
+      // the last sequence that begins at or before t
+      const uint32_t m = __ballot_sync(0xffffffffu, lane < p.B && __ldg(&p.cu_new[min(lane, p.B)]) <= t);
+      b = m ? 31 - __clz(m) : 0;
+    } else {
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(&p.cu_new[mid]) <= t) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
     }
-    b = lo;
   }
   const NewRows rows = new_rows(p, b, false);
   if (t < rows.t0 || t >= rows.t0 + rows.m) return;   // behind the last sequence, or skipped
-  const LaneDims ld = lane_dims(l, p.cos_sin ? p.rot : 0, p.interleaved != 0);
+  const LaneDims ld = lane_dims<W>(l, p.cos_sin ? p.rot : 0, p.interleaved != 0);
   const T* src = static_cast<const T*>(p.q) + (size_t)t * p.q_stride;
   T* dst = static_cast<T*>(p.q_out) + (size_t)t * p.Hq * D;
-  float xa[kHeadsPerItem][4], xb[kHeadsPerItem][4];
+  float c[W], s[W];
+  if (ld.turn) load_angles<W>(p, rows.first + t - rows.t0, l, c, s);
+  for (int h0 = part * per + lane / LPR; h0 < h_end; h0 += U * RPW) {
+    Raw<T, W> ra[U], rb[U];
 #pragma unroll
-  for (int i = 0; i < kHeadsPerItem; ++i) {
-    if (h0 + i < p.Hq) {
-      load4<T>(src + (h0 + i) * D + ld.a, xa[i]);
-      load4<T>(src + (h0 + i) * D + ld.b, xb[i]);
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * RPW;
+      if (h < h_end) {
+        ra[i].load(src + h * D + ld.a);
+        rb[i].load(src + h * D + ld.b);
+      }
     }
-  }
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ld.turn) {
-    const float4* cs = reinterpret_cast<const float4*>(
-        p.cos_sin + (size_t)(rows.first + t - rows.t0) * p.rot + 4 * l);
-    c = __ldg(cs);
-    s = __ldg(cs + p.rot / 8);
-  }
 #pragma unroll
-  for (int i = 0; i < kHeadsPerItem; ++i) {
-    if (h0 + i < p.Hq) {
-      if (ld.turn) turn_pairs(xa[i], xb[i], c, s, ld.adjacent);
-      store4(dst + (h0 + i) * D + ld.a, xa[i]);
-      store4(dst + (h0 + i) * D + ld.b, xb[i]);
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * RPW;
+      if (h < h_end) {
+        float xa[W], xb[W];
+        ra[i].values(xa);
+        rb[i].values(xb);
+        if (ld.turn) turn_pairs<W>(xa, xb, c, s, p.interleaved != 0);
+        store_row<W>(dst + h * D + ld.a, xa);
+        store_row<W>(dst + h * D + ld.b, xb);
+      }
     }
   }
 }
 
-template <typename T, int CODE, int D, int ITERS>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_constant__ Q8AppendParams p,
-                                                             int n_items) {
+template <typename T, int CODE, int D, int W, int ITERS>
+__global__ void __launch_bounds__(kThreads, ITERS > 4 ? 2 : 4) q8_append_kernel(const __grid_constant__ Q8AppendParams p,
+                                                             int n_items, int q_parts) {
   pdl_launch_dependents();
   pdl_wait();
-  if ((int)blockIdx.x < n_items) append_block<T, CODE, D, ITERS>(p, blockIdx.x);
-  else rotate_q<T, D>(p, (int)blockIdx.x - n_items);
+  if ((int)blockIdx.x < n_items) append_block<T, CODE, D, W, ITERS>(p, blockIdx.x);
+  else rotate_q<T, D, W>(p, (int)blockIdx.x - n_items, q_parts);
 }
 
-template <typename T, int CODE, int D>
+template <typename T, int CODE, int D, int W>
 cudaError_t launch_t(const Q8AppendParams& p, cudaStream_t st) {
-  constexpr int RPI = kThreads / (D / 8);
+  constexpr int LPR = D / (2 * W), RPI = kThreads / LPR, RPW = 32 / LPR;
   const int page = 1 << p.c.page_log2;
   // blocks with new rows: one a sequence, or at most T / page + 2 B (and T)
   long long blocks = p.B;
   if (p.cu_new) blocks = std::min<long long>((long long)p.T / page + 2LL * p.B, p.T);
   const long long items = blocks * 2 * p.Hkv;
-  const int parts = (p.Hq + kHeadsPerItem - 1) / kHeadsPerItem;
-  const long long qctas = p.q ? ((long long)p.T * parts + RPI - 1) / RPI : 0;
+  // a warp a token, or fewer heads a warp while the tokens are too few to fill the GPU
+  int parts = 1;
+  while (parts * RPW < p.Hq && (long long)p.T * parts < 4096) parts *= 2;
+  const long long qctas = p.q ? ((long long)p.T * parts + kWarps - 1) / kWarps : 0;
   if (items + qctas == 0) return cudaSuccess;
   if (items + qctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(items + qctas));
   const int need = p.cu_new ? (page + RPI - 1) / RPI : 1;
   cudaError_t e;
-  if (need <= 1) e = launch_pdl(q8_append_kernel<T, CODE, D, 1>, grid, dim3(kThreads), 0, st, p, (int)items);
-  else if (need <= 4) e = launch_pdl(q8_append_kernel<T, CODE, D, 4>, grid, dim3(kThreads), 0, st, p, (int)items);
-  else e = launch_pdl(q8_append_kernel<T, CODE, D, 8>, grid, dim3(kThreads), 0, st, p, (int)items);
+  if (need <= 1) e = launch_pdl(q8_append_kernel<T, CODE, D, W, 1>, grid, dim3(kThreads), 0, st, p, (int)items, parts);
+  else if (need <= 2) e = launch_pdl(q8_append_kernel<T, CODE, D, W, 2>, grid, dim3(kThreads), 0, st, p, (int)items, parts);
+  else if (need <= 4) e = launch_pdl(q8_append_kernel<T, CODE, D, W, 4>, grid, dim3(kThreads), 0, st, p, (int)items, parts);
+  else if constexpr (RPI * 4 < 128) e = launch_pdl(q8_append_kernel<T, CODE, D, W, 8>, grid, dim3(kThreads), 0, st, p, (int)items, parts);
+  else e = cudaErrorInvalidValue;
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 template <typename T, int CODE>
 cudaError_t launch_c(const Q8AppendParams& p, int D, cudaStream_t st) {
-  return D == 128 ? launch_t<T, CODE, 128>(p, st) : launch_t<T, CODE, 64>(p, st);
+  if constexpr (sizeof(T) == 2) {
+    if (p.rot % 16 == 0) return D == 128 ? launch_t<T, CODE, 128, 8>(p, st) : launch_t<T, CODE, 64, 8>(p, st);
+  }
+  return D == 128 ? launch_t<T, CODE, 128, 4>(p, st) : launch_t<T, CODE, 64, 4>(p, st);
 }
 
 }  // namespace
