@@ -32,7 +32,7 @@ lychee_status check_q8_shape(const lychee_q8_shape* s) {
   if ((long long)s->B * s->Hq >= (1LL << 24)) return LYCHEE_ERR_UNSUPPORTED;
   // slabs, over all sequences and heads, are counted in 32 bits too
   const long long n_max = (long long)s->max_pages * s->page;
-  if ((long long)s->B * s->Hkv * ((n_max + kQ8Tile - 1) / kQ8Tile) * (kQ8Tile / kQ8Slab) > 0x7fffffffLL)
+  if ((long long)s->B * s->Hkv * ((n_max + kQ8Tile - 1) / kQ8Tile) * (kQ8Tile / kQ8Slab + 1) > 0x7fffffffLL)
     return LYCHEE_ERR_UNSUPPORTED;
   return LYCHEE_OK;
 }

@@ -57,6 +57,7 @@ constexpr int kWarps = kQ8Warps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = kQ8Stages;
 constexpr int kRows = kQ8Slab;       // rows of a slab: two halves of 16, the M of the products
+constexpr int kSegCost = 1;          // what a segment costs beside its slabs, in slabs
 constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
 constexpr float kRefSlack = 15.f;    // and moves when a weight passes it by more than this
 constexpr uint32_t kAbsent = 0xffffffffu;  // of a slab's rows: none
@@ -166,7 +167,11 @@ struct Cfg {
   static constexpr int WARP_AUX = kStages * AUX + 32;    // and the stages' mbarriers
   static constexpr int OFF_AUX = kWarps * kStages * DATA;
   static constexpr int STATE = G * (D + 2);              // floats of a state: m[G], l[G], acc[G][D]
-  static constexpr int SMEM = OFF_AUX + kWarps * WARP_AUX + 1024;   // + alignment slack
+  // the states that warps end on their way: behind that where they fit (else in the
+  // workspace); the block's other shared variables take less than 768 bytes
+  static constexpr int OFF_ENDED = OFF_AUX + kWarps * WARP_AUX;
+  static constexpr bool kEndedHere = OFF_ENDED + kWarps * STATE * 4 + 1024 + 768 <= 227 * 1024;
+  static constexpr int SMEM = OFF_ENDED + (kEndedHere ? kWarps * STATE * 4 : 0) + 1024;   // + alignment slack
   static_assert(WARP_AUX % 16 == 0 && kStages * 8 <= 32, "aligned");
   static_assert(DATA / 2 % 1024 == 0 || D == 64, "swizzled rows on 1024-byte (D = 64: 512-byte) boundaries");
   static_assert(kWarps * STATE * 4 <= OFF_AUX, "the states are merged where the rings were");
@@ -701,21 +706,30 @@ struct Chain {
 // What the ranges are counted in: sequences (dense: the slabs of all their KV
 // heads), or the tiles of the segments (hybrid).  (The host keeps all slabs of a
 // call below 2^31.)
+// Ranges are equal in units: a slab is one, and the beginning of a segment
+// (queries to load, an output to write) kSegCost more before its first slab.
 template <bool HYB>
 __device__ __forceinline__ int item_slabs(const Q8AttnParams& p, int i, int n_items) {
   if (i >= n_items) return 0;
   if (HYB) return (__ldcg(&p.tile_rows[i]) + kRows - 1) / kRows;
   return (min(max(__ldg(&p.seqlens[i]), 0), p.N_max) + kRows - 1) / kRows * p.Hkv;
 }
-// Slab `rel` of item i, which has `slabs`.
 template <bool HYB>
-__device__ __forceinline__ Start start_at(const Q8AttnParams& p, int slabs, int i, int rel) {
+__device__ __forceinline__ int item_units(const Q8AttnParams& p, int slabs) {
+  return HYB || slabs == 0 ? slabs : slabs + kSegCost * p.Hkv;
+}
+// The first slab at or behind unit `rel` of item i, which has `slabs` (rel may lie
+// at its end: then the next item's first); `index` gets its number in the item.
+template <bool HYB>
+__device__ __forceinline__ Start start_at(const Q8AttnParams& p, int slabs, int i, int rel, int& index) {
   if (HYB) {
     const int seg = i / p.ntiles;
+    index = rel;
     return Start{seg, i - seg * p.ntiles, rel};
   }
-  const int len = slabs / p.Hkv, g = rel / len;
-  return Start{i * p.Hkv + g, 0, rel - g * len};
+  const int len = slabs / p.Hkv, g = rel / (len + kSegCost), slab = max(rel - g * (len + kSegCost) - kSegCost, 0);
+  index = g * len + slab;
+  return Start{i * p.Hkv + g, 0, slab};
 }
 
 constexpr int kEntries = 2 * kWarps;   // states in a CTA's merge: each warp's ended one, then its open one
@@ -726,9 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ int s_wsum[kWarps];
-  __shared__ int3 s_at[kWarps];
+  __shared__ int4 s_at[kWarps + 1];     // per warp, and for the range's end: item, its units before, slabs, slabs before
+  __shared__ int s_index[kWarps + 1];   // slabs of the call before the warp's first one
   __shared__ WarpEnd s_end[kWarps];
-  __shared__ float s_f[G][32], s_l[G][32], s_m[G][32];
+  __shared__ Start s_start[kWarps];
   __shared__ uint32_t s_first, s_valid;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
@@ -748,27 +763,46 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   const int n_items = HYB ? p.B * p.Hkv * p.ntiles : p.B;
   Start s0{0, 0, 0};
   int mine = 0;
-  // the ranges of [0, total): per CTA, at least kQ8MinSlabs a warp, then per warp
+  // the ranges of [0, total) units: per CTA, at least kQ8MinSlabs a warp, then per warp
   int c0 = 0, c1 = 0, per_warp = 1;
   auto cut_ranges = [&](int total) {
     const int per_cta = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kQ8MinSlabs * kWarps);
     c0 = (int)min((long long)total, (long long)per_cta * blockIdx.x);
     c1 = (int)min((long long)total, (long long)c0 + per_cta);
     per_warp = max((c1 - c0 + kWarps - 1) / kWarps, 1);
-    const int w0 = min(c1, c0 + per_warp * warp);
-    mine = min(c1 - w0, per_warp);
   };
-  // hands the item to the warps whose ranges begin in [lo, lo + slabs)
-  auto place = [&](int slabs, int i, int lo) {
-    const int hi = lo + slabs;
-    if (slabs > 0 && hi > c0 && lo < c1) {
-      int w = lo > c0 ? (lo - c0 + per_warp - 1) / per_warp : 0;
-      for (; w < kWarps && c0 + w * per_warp < min(hi, c1); ++w) s_at[w] = make_int3(i, lo, slabs);
+  // Hands the item to the warps whose ranges begin among its units [lo, lo + units),
+  // warp kWarps standing for the end of the CTA's range; `before`: slabs before it.
+  auto place = [&](int units, int slabs, int i, int lo, int before) {
+    const int hi = lo + units;
+    if (units > 0 && hi > c0 && lo <= c1) {
+      for (int w = lo > c0 ? (lo - c0 + per_warp - 1) / per_warp : 0; w <= kWarps; ++w) {
+        const int u = w < kWarps ? min(c0 + w * per_warp, c1) : c1;
+        if (u >= hi) break;
+        if (u >= lo) s_at[w] = make_int4(i, lo, slabs, before);
+      }
     }
   };
-  auto my_start = [&]() {
+  // (whoever finds no item begins at the call's end)
+  auto my_start = [&](int total, int all_slabs) {
+    if (tid <= kWarps) {
+      const int u = tid < kWarps ? min(c0 + tid * per_warp, c1) : c1;
+      if (u >= total) s_at[tid].x = -1;
+    }
     __syncthreads();
-    if (mine > 0) s0 = start_at<HYB>(p, s_at[warp].z, s_at[warp].x, c0 + warp * per_warp - s_at[warp].y);
+    if (lane == 0 || (warp == 0 && lane == 1)) {
+      const int w = lane == 0 ? warp : kWarps;
+      const int u = w < kWarps ? min(c0 + w * per_warp, c1) : c1;
+      const int4 at = s_at[w];
+      int index = 0;
+      Start st{0, 0, 0};
+      if (at.x >= 0) st = start_at<HYB>(p, at.z, at.x, u - at.y, index);
+      s_index[w] = at.x >= 0 ? at.w + index : all_slabs;
+      if (w < kWarps) s_start[w] = st;
+    }
+    __syncthreads();
+    s0 = s_start[warp];
+    mine = s_index[warp + 1] - s_index[warp];
   };
   // exclusive prefix of v over the CTA's threads; `sum` gets the total
   auto scan = [&](int v, int& sum) {
@@ -800,27 +834,42 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       s0.slab = w0;
     }
   } else if (n_items <= kThreads) {
-    const int slabs = item_slabs<HYB>(p, tid, n_items);
-    int total;
-    const int lo = scan(slabs, total);
-    cut_ranges(total);
-    place(slabs, tid, lo);
-    my_start();
-  } else {
-    int mine_all = 0, total = 0;
-    for (int i = tid; i < n_items; i += kThreads) mine_all += item_slabs<HYB>(p, i, n_items);
-    scan(mine_all, total);
-    cut_ranges(total);
-    int before = 0;
-    for (int i0 = 0; i0 < n_items && before < c1; i0 += kThreads) {
-      const int slabs = item_slabs<HYB>(p, i0 + tid, n_items);
-      __syncthreads();   // the last round's sums were read
-      int round;
-      const int lo = before + scan(slabs, round);
-      place(slabs, i0 + tid, lo);
-      before += round;
+    const int slabs = item_slabs<HYB>(p, tid, n_items), units = item_units<HYB>(p, slabs);
+    int total, all_slabs;
+    const int lo = scan(units, total);
+    int before = lo;
+    all_slabs = total;
+    if (!HYB) {
+      __syncthreads();   // the sums were read
+      before = scan(slabs, all_slabs);
     }
-    my_start();
+    cut_ranges(total);
+    place(units, slabs, tid, lo, before);
+    my_start(total, all_slabs);
+  } else {
+    int my_units = 0, my_slabs = 0, total, all_slabs;
+    for (int i = tid; i < n_items; i += kThreads) {
+      const int slabs = item_slabs<HYB>(p, i, n_items);
+      my_slabs += slabs;
+      my_units += item_units<HYB>(p, slabs);
+    }
+    scan(my_units, total);
+    __syncthreads();     // the sums were read
+    scan(my_slabs, all_slabs);
+    cut_ranges(total);
+    int units_before = 0, slabs_before = 0;
+    for (int i0 = 0; i0 < n_items && units_before <= c1; i0 += kThreads) {
+      const int slabs = item_slabs<HYB>(p, i0 + tid, n_items), units = item_units<HYB>(p, slabs);
+      int round_units, round_slabs;
+      __syncthreads();
+      const int lo = units_before + scan(units, round_units);
+      __syncthreads();
+      const int before = slabs_before + scan(slabs, round_slabs);
+      place(units, slabs, i0 + tid, lo, before);
+      units_before += round_units;
+      slabs_before += round_slabs;
+    }
+    my_start(total, all_slabs);
   }
   if (!HYB) {
     // sequences of no rows give zeros
@@ -831,6 +880,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   // ---- the warp's slabs
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::DATA;
   WarpEnd end{-1, -1, 0};
+  auto ended_at = [&](int w) {
+    return C::kEndedHere ? reinterpret_cast<float*>(smem + C::OFF_ENDED) + w * C::STATE
+                         : p.scratch + ((size_t)blockIdx.x * kWarps + w) * C::STATE;
+  };
   using Wk = Warp<T, CODE, D, G, HYB>;
   Wk wk(p, ring, smem_u32(smem) + C::OFF_AUX + warp * C::WARP_AUX);
   if (mine > 0) {
@@ -860,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
       if ((int)hd.x != seg) {
         if (began) wk.write_out(seg);
         else {
-          wk.write_state(p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE);
+          wk.write_state(ended_at(warp));
           end.ended = seg;
         }
         began = true;
@@ -887,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     if (done && began) wk.write_out(seg);
     else {
       // (an open state goes where the warp's ring was)
-      wk.write_state(done ? p.scratch + ((size_t)blockIdx.x * kWarps + warp) * C::STATE
+      wk.write_state(done ? ended_at(warp)
                           : reinterpret_cast<float*>(smem + warp * kStages * C::DATA));
       if (done) end.ended = seg;
       else {
@@ -899,6 +952,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   if (lane == 0) s_end[warp] = end;
   __syncthreads();
 
+  float (*s_f)[32] = reinterpret_cast<float (*)[32]>(smem + C::OFF_AUX), (*s_l)[32] = s_f + G, (*s_m)[32] = s_l + G;
+  static_assert(3 * G * 32 * 4 <= kWarps * C::WARP_AUX, "factors where the warps' headers were");
+
   // ---- merge.  Entry 2w is warp w's ended state (of a segment that began before the
   // warp), entry 2w + 1 its open one.  Valid entries of one segment are neighbours:
   // a chain.  A chain's factors first (one warp a head), then its columns.
@@ -909,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     float m = kNoRef, l = 0.f;
     if (valid) {
       const float* s = lane & 1 ? reinterpret_cast<const float*>(smem + (lane >> 1) * kStages * C::DATA)
-                                : p.scratch + ((size_t)blockIdx.x * kWarps + (lane >> 1)) * C::STATE;
+                                : ended_at(lane >> 1);
       m = s[h];
       l = s[G + h];
     }
@@ -976,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
           const int k = __ffs(left) - 1;
           left &= left - 1;
           const float* s = (k & 1 ? reinterpret_cast<const float*>(smem + (k >> 1) * kStages * C::DATA)
-                                  : p.scratch + ((size_t)blockIdx.x * kWarps + (k >> 1)) * C::STATE) + 2 * G + col;
+                                  : ended_at(k >> 1)) + 2 * G + col;
           f[u] = s_f[h][k];
           x[u] = *reinterpret_cast<const float2*>(s);
           y[u] = *reinterpret_cast<const float2*>(s + 2);
