@@ -115,8 +115,8 @@ __device__ __forceinline__ void load_angles(const Q8AppendParams& p, int pos, in
   const float* at = p.cos_sin + (size_t)pos * p.rot + W * j;
 #pragma unroll
   for (int i = 0; i < W / 4; ++i) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(at) + i);
-    const float4 y = __ldg(reinterpret_cast<const float4*>(at + p.rot / 2) + i);
+    const float4 x = *(reinterpret_cast<const float4*>(at) + i);
+    const float4 y = *(reinterpret_cast<const float4*>(at + p.rot / 2) + i);
     c[4 * i] = x.x; c[4 * i + 1] = x.y; c[4 * i + 2] = x.z; c[4 * i + 3] = x.w;
     s[4 * i] = y.x; s[4 * i + 1] = y.y; s[4 * i + 2] = y.z; s[4 * i + 3] = y.w;
   }
@@ -149,11 +149,11 @@ struct NewRows {
 };
 __device__ __forceinline__ NewRows new_rows(const Q8AppendParams& p, int b, bool flag) {
   NewRows r{b, 1, 0};
-  const int n = __ldg(&p.seqlens[b]);
+  const int n = p.seqlens[b];
   bool ok = true;
   if (p.cu_new) {
-    r.t0 = __ldg(&p.cu_new[b]);
-    const int t1 = __ldg(&p.cu_new[b + 1]);
+    r.t0 = p.cu_new[b];
+    const int t1 = p.cu_new[b + 1];
     ok = r.t0 >= 0 && t1 >= r.t0 && t1 <= p.T;
     r.m = ok ? t1 - r.t0 : 0;
   } else if (n == 0) {
@@ -254,7 +254,7 @@ __device__ __forceinline__ void append_block(const Q8AppendParams& p, int item) 
   if (b < 0) return;
   const int page_len = 1 << p.c.page_log2, base = j << p.c.page_log2;
   const int lo = max(rows.first, base), hi = min(rows.first + rows.m, base + page_len);
-  const int page = __ldg(&p.c.table[(size_t)b * p.c.max_pages + j]);
+  const int page = p.c.table[(size_t)b * p.c.max_pages + j];
   if (page < 0 || page >= p.c.num_pages) {
     if (threadIdx.x == 0) flag_error(p.err, kErrBadIndex);
     return;
@@ -362,13 +362,13 @@ __device__ __forceinline__ void rotate_q(const Q8AppendParams& p, int cta, int p
   if (p.cu_new) {
     if (p.B <= 32) {
       // the last sequence that begins at or before t
-      const uint32_t m = __ballot_sync(0xffffffffu, lane < p.B && __ldg(&p.cu_new[min(lane, p.B)]) <= t);
+      const uint32_t m = __ballot_sync(0xffffffffu, lane < p.B && p.cu_new[min(lane, p.B)] <= t);
       b = m ? 31 - __clz(m) : 0;
     } else {
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(&p.cu_new[mid]) <= t) lo = mid;
+        if (p.cu_new[mid] <= t) lo = mid;
         else hi = mid;
       }
       b = lo;

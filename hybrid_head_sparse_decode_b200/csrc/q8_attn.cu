@@ -7,9 +7,11 @@
 // (or over the head's set), out = sum_j p_j sv c'_j.  A sequence of no rows and an
 // empty set give zeros.  Both products run on the tensor cores without a second
 // rounding of the cache, and take the scales afterwards.
-// The codes become halves (exact: both code types fit 11 bits); the 8-bit forms of
-// mma.sync are no use here, the compiler turns them into the same conversions and
-// more (a slab then took 490 instructions against 330).  q is scaled by a power of
+//
+// Numbers.  The codes become halves (exact: both code types fit 11 bits).  (The
+// 8-bit form of mma.sync with q in two parts took 490 instructions for 16 rows
+// against 415: the compiler turns it into the same conversions and twice the
+// products.)  q is scaled by a power of
 // two that brings its largest magnitude to [2^13, 2^14): a bf16 is then a half
 // exactly down to 2^-27 of the largest, and an fp32 is held in two halves (22
 // bits).  The weight that multiplies the values' codes is w_j = p_j sv_j; it is what
@@ -28,23 +30,32 @@
 // group uses).  A warp works alone: it brings its slabs into a ring of its own in
 // shared memory and runs the G heads of the group over each slab at once; no
 // barrier joins the warps before the end.  A full slab is 32 consecutive rows: a
-// TMA box of K and one of V (two each when pages have 16 rows).  The rows of a sparse head's set, and a
-// slab cut by the sequence's end, come row by row (cp.async, absent rows as
-// zeros).  At the end the CTA merges its warps' states of a segment, writes what
+// TMA box of K and one of V (two each when pages have 16 rows).  The rows of sparse
+// heads' sets, and a slab cut by the sequence's end, come row by row (cp.async,
+// absent rows as zeros).  At the end the CTA merges its warps' states of a segment, writes what
 // is complete and leaves at most two states open: of a segment that began in an
 // earlier CTA and of one that goes on in a later CTA.  The second kernel merges
 // those.  When there are fewer segments than CTAs and they are short, every
 // segment is one CTA's and nothing is left to merge.  All sums have a fixed order.
 //
 // Layouts.  Rows lie in shared memory with the TMA's swizzle (16-byte pieces of a
-// row XORed with its number).  S = K q^T as m16n8k16 with 16 of the slab's rows as M: a lane takes 16-byte piece c (c = lane % 4) of its
-// two rows; which dimension a k index means is free as long as q agrees, so a
+// row XORed with its number).  S = K q^T as m16n8k16 with 16 of the slab's rows as M:
+// a lane takes 16-byte piece c (c = lane % 4) of its two rows; which dimension a k index means is free as long as q agrees, so a
 // row's words convert to A fragments in place.  O^T = V^T P with the
 // dimensions as M: a lane takes piece lane / 4 of four rows; interleaving the bytes
 // of two rows gives the pairs along k that A wants.  Which row stands at which index
 // of M and k is free too: index i is row i ^ 4 (i & 1), which makes both reads
 // free of bank conflicts.  P moves from the accumulator layout to B by a
 // transpose of 8x8 halves (movmatrix).
+//
+// Bound by memory where there is enough to read: 131072 positions of 8 KV heads of
+// 128 (268 MB) take 48.8 us, of which the slabs 38 (7.1 TB/s), finding the ranges and
+// the first rows 5, merging and the second launch 5.  Next to it stand the
+// instructions (a 16-row step took 415 of them in slabs of 16, and less in slabs of
+// 32, whose bookkeeping is shared): int8 codes, two more per pair to become halves,
+// stay 8 % above the copy rate's time.  12 warps with rings of two slabs and 168
+// registers (49.0 / 96 us on that case / a batch of 64 of up to 8191 in int8) beat 8
+// with rings of three (49.5 / 104) and 16 of 16-row slabs (51.6 / 102).
 #include <algorithm>
 
 #include "q8.cuh"
@@ -57,12 +68,14 @@ constexpr int kWarps = kQ8Warps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = kQ8Stages;
 constexpr int kRows = kQ8Slab;       // rows of a slab: two halves of 16, the M of the products
-constexpr int kSegCost = 1;          // what a segment costs beside its slabs, in slabs
+// What a segment costs beside its slabs, in slabs (256 sequences of up to 600: 40.3 us
+// without it, 34.8 with 1, 35.2 with 2).
+constexpr int kSegCost = 1;
 constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
 constexpr float kRefSlack = 15.f;    // and moves when a weight passes it by more than this
 constexpr uint32_t kAbsent = 0xffffffffu;  // of a slab's rows: none
 constexpr float kNoRef = -1e30f;     // no row yet (finite: differences of two stay numbers)
-constexpr uint32_t kFullSlab = 1u << 29;   // stage header: sixteen rows of one page, one scale
+constexpr uint32_t kFullSlab = 1u << 29;   // stage header: consecutive rows, a scale a half
 constexpr uint32_t kAllHeads = 1u << 30;   // ... and every head uses every row
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -100,7 +113,7 @@ __device__ __forceinline__ float fast_log2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Rows y .. y + 15 of the map's array, all of their bytes, to dst in the map's swizzle.
+// A box of rows from y on of the map's array, all of their bytes, to dst in the map's swizzle.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int y, uint32_t bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
@@ -111,9 +124,9 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-               "{%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
@@ -226,7 +239,7 @@ struct Warp {
     seg = seg_;
     b = seg / p.Hkv;
     g = seg - b * p.Hkv;
-    n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
+    n = min(max(p.seqlens[b], 0), p.N_max);
     at = 0;
     if (HYB) {
       int kept = 0;
@@ -278,7 +291,7 @@ struct Warp {
     } else {
       // (a page of 16 positions is half a slab: odd lanes take the second half's)
       const int pos0 = tile * kQ8Tile + kRows * at, pos = pos0 + 16 * (lane & 1);
-      pre = __ldg(&p.c.table[(size_t)b * p.c.max_pages + ((pos < n ? pos : pos0) >> p.c.page_log2)]);
+      pre = p.c.table[(size_t)b * p.c.max_pages + ((pos < n ? pos : pos0) >> p.c.page_log2)];
       if (HYB && mixed) {
         pre_m = 0xffffffffu;
         if (lane < G && !retrieval(g * G + lane))
@@ -685,8 +698,8 @@ struct Warp {
 
 // What a warp leaves for the CTA's merge.
 struct WarpEnd {
-  int ended;     // segment that began before the warp and ended in it (its state in global memory), or -1
-  int open;      // segment still open at the warp's end (its state in shared memory), or -1
+  int ended;     // segment that began before the warp and ended in it, or -1
+  int open;      // segment still open at the warp's end, or -1
   int began;     // the open segment began in this warp
 };
 
@@ -704,15 +717,15 @@ struct Chain {
 };
 
 // What the ranges are counted in: sequences (dense: the slabs of all their KV
-// heads), or the tiles of the segments (hybrid).  (The host keeps all slabs of a
-// call below 2^31.)
+// heads), or the tiles of the segments (hybrid).  The host keeps all slabs of a call
+// below 2^31.
 // Ranges are equal in units: a slab is one, and the beginning of a segment
 // (queries to load, an output to write) kSegCost more before its first slab.
 template <bool HYB>
 __device__ __forceinline__ int item_slabs(const Q8AttnParams& p, int i, int n_items) {
   if (i >= n_items) return 0;
   if (HYB) return (__ldcg(&p.tile_rows[i]) + kRows - 1) / kRows;
-  return (min(max(__ldg(&p.seqlens[i]), 0), p.N_max) + kRows - 1) / kRows * p.Hkv;
+  return (min(max(p.seqlens[i], 0), p.N_max) + kRows - 1) / kRows * p.Hkv;
 }
 template <bool HYB>
 __device__ __forceinline__ int item_units(const Q8AttnParams& p, int slabs) {
@@ -756,9 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   // ---- how many slabs there are, and where each warp's begin
   if (blockIdx.x == 0)
     for (int b = tid; b < p.B; b += kThreads) {
-      const int n = __ldg(&p.seqlens[b]);
+      const int n = p.seqlens[b];
       if (n < 0 || n > p.N_max) flag_error(p.err, kErrBadSeqlen);
-      if (HYB && p.k_per_seq && n > 0 && __ldg(&p.k_per_seq[b]) < 1) flag_error(p.err, kErrBadBudget);
+      if (HYB && p.k_per_seq && n > 0 && p.k_per_seq[b] < 1) flag_error(p.err, kErrBadBudget);
     }
   const int n_items = HYB ? p.B * p.Hkv * p.ntiles : p.B;
   Start s0{0, 0, 0};
@@ -827,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     // segment blockIdx.x is this CTA's
     if ((int)blockIdx.x < p.B * p.Hkv) {
       // (hybrid: it has one tile, its rows below kQ8WholeMax)
-      const int rows = HYB ? __ldcg(&p.tile_rows[blockIdx.x]) : min(max(__ldg(&p.seqlens[blockIdx.x / p.Hkv]), 0), p.N_max);
+      const int rows = HYB ? __ldcg(&p.tile_rows[blockIdx.x]) : min(max(p.seqlens[blockIdx.x / p.Hkv], 0), p.N_max);
       const int total = (rows + kRows - 1) / kRows, per = (total + kWarps - 1) / kWarps, w0 = min(total, per * warp);
       mine = min(total, w0 + per) - w0;
       s0.seg = blockIdx.x;
@@ -874,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   if (!HYB) {
     // sequences of no rows give zeros
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-      if (__ldg(&p.seqlens[b]) <= 0)
+      if (p.seqlens[b] <= 0)
         for (int i = tid; i < p.Hq * D; i += kThreads) store1(static_cast<T*>(p.out) + (size_t)b * p.Hq * D + i, 0.f);
   }
   // ---- the warp's slabs
@@ -940,8 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     if (done && began) wk.write_out(seg);
     else {
       // (an open state goes where the warp's ring was)
-      wk.write_state(done ? ended_at(warp)
-                          : reinterpret_cast<float*>(smem + warp * kStages * C::DATA));
+      wk.write_state(done ? ended_at(warp) : reinterpret_cast<float*>(smem + warp * kStages * C::DATA));
       if (done) end.ended = seg;
       else {
         end.open = seg;
@@ -1132,6 +1144,8 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
 int attn_grid(int sms) { return std::min(sms, kQ8MaxCtas); }
 // A segment per CTA when that leaves no segment over and none is longer than
 // kQ8WholeMax positions: nothing is left open, and one launch less than splitting.
+// (8 KV heads of 128, one sequence: 512 positions 7.0 us against 10.1 split, 1024 9.4
+// against 10.2, 2048 14.0 against 10.4; eight sequences of 1024: 9.8 against 12.3.)
 bool takes_whole(const Q8AttnParams& p, int grid) {
   return (long long)p.B * p.Hkv <= grid && p.N_max <= kQ8WholeMax;
 }

@@ -44,7 +44,7 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seg = item / p.ntiles, tile = item - seg * p.ntiles;
   const int b = seg / p.Hkv, g = seg - b * p.Hkv;
-  const int n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
+  const int n = min(max(p.seqlens[b], 0), p.N_max);
   const int base = tile * kQ8Tile, rows = min(max(n - base, 0), kQ8Tile);
   uint32_t sparse = 0;                        // bit t: head t of the group is sparse
 #pragma unroll
@@ -83,7 +83,7 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
 #pragma unroll
         for (int i = 0; i < kSamples; ++i) {
           const int at = lo + (64 * i + j + 1) * step - 1;
-          v[i] = at < hi ? (uint32_t)__ldg(&row[at]) : 0xffffffffu;
+          v[i] = at < hi ? (uint32_t)row[at] : 0xffffffffu;
         }
 #pragma unroll
         for (int i = 0; i < kSamples; ++i) below += v[i] < target;
@@ -109,7 +109,7 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
     for (int e0 = s_lo[2 * t] + kBatch * (tid % per); e0 < to; e0 += kBatch * per) {
       int at[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) at[i] = e0 + i < to ? __ldg(&row[e0 + i]) - base : -1;
+      for (int i = 0; i < kBatch; ++i) at[i] = e0 + i < to ? row[e0 + i] - base : -1;
       // neighbours share a word: collect them before the atomic
       uint32_t m = 0;
 #pragma unroll
@@ -171,7 +171,7 @@ __device__ __forceinline__ void build_tile(const Q8AttnParams& p, int item) {
   const int32_t* table = p.c.table + (size_t)b * p.c.max_pages;
 #pragma unroll 4
   for (int i = tid; i < total; i += kThreads) {
-    const int pos = base + s_off[i], page = __ldg(&table[pos >> p.c.page_log2]);
+    const int pos = base + s_off[i], page = table[pos >> p.c.page_log2];
     const bool ok = page >= 0 && page < p.c.num_pages;
     if (!ok) flag_error(p.err, kErrBadIndex);
     // (no page: an absent row that no head uses)
@@ -192,7 +192,7 @@ __device__ __forceinline__ void hand_on(const Q8AttnParams& p, int item, int par
   __syncthreads();
   const int pair = item / parts, part = item - pair * parts;
   const int b = pair / p.n_sparse;
-  const int n = min(max(__ldg(&p.seqlens[b]), 0), p.N_max);
+  const int n = min(max(p.seqlens[b], 0), p.N_max);
   const size_t row = ((size_t)b * p.Hq + s_head[pair - b * p.n_sparse]) * p.k;
   const int32_t* in = p.idx_in + row;
   constexpr int N = 8;
@@ -204,8 +204,8 @@ __device__ __forceinline__ void hand_on(const Q8AttnParams& p, int item, int par
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = e0 + i * kThreads + threadIdx.x;
-      v[i] = e < end ? __ldg(&in[e]) : -1;
-      before[i] = lane == 0 && e > 0 && e < end ? __ldg(&in[e - 1]) : -1;
+      v[i] = e < end ? in[e] : -1;
+      before[i] = lane == 0 && e > 0 && e < end ? in[e - 1] : -1;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {

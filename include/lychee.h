@@ -316,9 +316,12 @@ LYCHEE_API lychee_status lychee_hardkuma_roles(const double* alpha, const double
  *          appended to (a common prefix).
  * Scales are powers of two 2^e, -60 <= e <= 60, as the append writes them.
  * Attention takes any positive finite scale within that range.
+ * e4m3's NaN codes are no values: the append writes none, and none may stand in a
+ * row that is attended to.  Rows behind a sequence's end may hold anything.
  *
  * Supported: G = Hq / Hkv in {1, 2, 4, 8}, Hq <= 128, d in {64, 128}, page in
- * {16, 32, 64, 128}, max_pages * page <= 2^24, num_pages * Hkv * page < 2^31.
+ * {16, 32, 64, 128}, max_pages * page <= 2^24, num_pages * Hkv * page < 2^31.  The table's capacity over
+ * all sequences, B * Hkv * max_pages * page, stays below 2^35.
  *
  * Conventions beyond those at the top of this file
  *   - A sequence may be empty (seqlens[b] == 0): its outputs are zeros, its
@@ -405,8 +408,10 @@ LYCHEE_API size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k);
  * out[b, h] = softmax(q . K_g^T / sqrt(d)) V_g over positions j < seqlens[b].
  *   q, out    device [B, Hq, d] dtype, 16-byte aligned
  *   workspace device, >= lychee_q8_workspace_size(s, 0) bytes, 256-byte aligned
- * Scores are exact products of the codes with q (bf16), or with q held in two
- * 11-bit parts (fp32), summed in fp32; softmax and sums are fp32. */
+ * Scores are exact products of the codes with q (bf16, down to 2^-27 of its largest
+ * element), or with q held in two 11-bit parts (fp32), summed in fp32; softmax and
+ * sums are fp32; the softmax weights are rounded to 11 bits (bf16) or held in two
+ * such parts (fp32). */
 LYCHEE_API lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q,
                                                const lychee_q8_cache* cache, const int32_t* seqlens,
                                                void* out, void* workspace, size_t workspace_bytes,

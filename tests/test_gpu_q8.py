@@ -331,6 +331,30 @@ def test_hybrid_long_and_sparse():
     run_hybrid([40000], 4, 4, 64, 128, BF, I8, [0, 1, 0, 1], [0.4, 0.002], budgets=[12000])
 
 
+def test_hybrid_many_tiles():
+    """More tiles than the attention's CTAs have threads: ranges are found in rounds."""
+    lens = [16384] + [50 + i for i in range(24)]
+    run_hybrid(lens, 4, 4, 64, 64, BF, I8, [0, 1, 0, 0], [0.1, 0.0, 0.5], budgets=[100] + [20] * 24, k=2000)
+    run_hybrid([0] * 5 + lens[::-1], 8, 4, 64, 64, BF, E4, [0, 0, 0, 0, 0, 1, 0, 0], [0.002, 0.3], budgets=[1] * 5 + [20] * 24 + [100],
+               k=5000)
+
+
+def test_hybrid_in_place():
+    """idx_out may be idx_in: sets of sparse heads stay, retrieval heads' are replaced."""
+    g = torch.Generator().manual_seed(5)
+    table, P = R.make_table(g, [3000], 32)
+    cache = to_dev(R.make_cache(g, P, 2, 32, 64, I8))
+    q = torch.randn(1, 8, 64, generator=g).to(BF).to(DEV)
+    seq = torch.tensor([3000], dtype=torch.int32, device=DEV)
+    idx = torch.rand(1, 8, 3000, generator=g).topk(700, dim=2).indices.sort(dim=2).values.int().to(DEV)
+    roles = [1, 0, 0, 0, 0, 0, 0, 0]
+    out, nxt = ops.hybrid_decode_attn_q8(q, cache, table.to(DEV), seq, roles, idx, 700)
+    same_buffer = idx.clone()
+    out2, nxt2 = ops.hybrid_decode_attn_q8(q, cache, table.to(DEV), seq, roles, same_buffer, 700, idx_out=same_buffer)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(nxt, nxt2) and nxt2 is same_buffer
+
+
 def test_hybrid_blocks():
     run_hybrid([700, 64, 1, 0, 95], 8, 2, 64, 32, BF, E4, [1, 0, 0, 0, 1, 1, 0, 0], [0.3], block=64,
                budgets=[256, 64, 64, 64, 64], k=256)
