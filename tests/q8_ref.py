@@ -78,12 +78,18 @@ def rows_of(store, scale, table_row, n):
     return x.permute(1, 0, 2, 3).reshape(store.shape[1], -1, store.shape[3])[:, :n]
 
 
+def scale_rows(scale, table_row, n, page):
+    """One sequence's scales, row by row [Hkv, n], in fp64."""
+    ids = table_row[:(n + page - 1) // page].long()
+    return scale[ids].double().T.repeat_interleave(page, 1)[:, :n]
+
+
 def attend(q, cache, table, seqlens, sets=None):
     """fp64 attention.  q [B, Hq, d]; sets: None, or sets[b][h] = None (every position) or a list.
     Returns out, the bound of the kernels' error, raw logits[b] [Hq, n], their error's bound[b] [Hq]."""
     k, v, ks, vs = cache
     B, Hq, d = q.shape
-    G = Hq // k.shape[1]
+    G, page = Hq // k.shape[1], k.shape[2]
     out = torch.zeros(B, Hq, d, dtype=torch.float64)
     tol = torch.zeros(B, Hq, d, dtype=torch.float64)
     raws, raw_tols = [], []
@@ -111,6 +117,10 @@ def attend(q, cache, table, seqlens, sets=None):
             # sums of one rounding per 16 rows and per merged state (2^-23 each)
             w = 2 * float(rt[h]) / math.sqrt(d) + 2.0 ** -21 + (2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -22)
             tol[b, h] = (w + (at.numel() / 16 + 64) * 2.0 ** -23) * spread + UNIT[q.dtype] * out[b, h].abs()
+            # a weight p sv multiplies codes as a half (or two) whose smallest step is 2^-24, the
+            # largest weight being 2^6 or more: each is off by at most 2^-25 2^-6 of the largest
+            sv = scale_rows(vs, table[b], n, page)[h // G][at]
+            tol[b, h] += 2.0 ** -31 * float((p * sv).max()) * (Vh.abs() / sv[:, None]).sum(0)
     return out, tol, raws, raw_tols
 
 
