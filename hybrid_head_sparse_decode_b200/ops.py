@@ -455,43 +455,43 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
     if dt not in _DT:
         raise TypeError(f"k_new must be torch.bfloat16 or torch.float32, got {dt}")
     index = _device_index("k_new", k_new)
-    tok = N.Q8Tokens()
-    tok.k_stride = _need_rows("k_new", k_new, dt, shape, dev, index)
-    tok.v_stride = _need_rows("v_new", v_new, dt, shape, dev, index)
-    tok.k, tok.v, tok.T = k_new.data_ptr(), v_new.data_ptr(), T
-    Hq = Hkv
+    k_stride = _need_rows("k_new", k_new, dt, shape, dev, index)
+    v_stride = _need_rows("v_new", v_new, dt, shape, dev, index)
+    Hq, q_stride, q_ptr, q_out_ptr = Hkv, 0, None, None
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be a tensor [T, Hq, d]")
         Hq = q.shape[1]
-        tok.q_stride = _need_rows("q", q, dt, (T, Hq, d), dev, index)
+        q_stride = _need_rows("q", q, dt, (T, Hq, d), dev, index)
         if q_out is None:
             q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
         else:
             _need("q_out", q_out, dt, (T, Hq, d), dev, index)
-        tok.q, tok.q_out = q.data_ptr(), q_out.data_ptr()
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     sh, ptrs, B, cache_heads = _q8_cache(cache, block_table, seqlens, Hq, d, dt, dev, index)
     if cache_heads != Hkv:
         raise ValueError(f"k_new has {Hkv} heads, the cache {cache_heads}")
+    cu_ptr = cs_ptr = err = None
     if cu_new is not None:
         _need("cu_new", cu_new, torch.int32, (B + 1,), dev, index)
-        tok.cu_new = cu_new.data_ptr()
+        cu_ptr = cu_new.data_ptr()
     elif T != B:
         raise ValueError(f"without cu_new there is one token a sequence: got {T} for {B}")
+    n_pos = rot = 0
     if cos_sin is not None:
         if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be a tensor [n_pos, rot]")
-        _need("cos_sin", cos_sin, torch.float32, cos_sin.shape, dev, index)
-        tok.n_pos, tok.rot = cos_sin.shape
-        tok.cos_sin = cos_sin.data_ptr()
-    tok.interleaved = 1 if interleaved else 0
-    err = None
+        n_pos, rot = cos_sin.shape
+        _need("cos_sin", cos_sin, torch.float32, (n_pos, rot), dev, index)
+        cs_ptr = cos_sin.data_ptr()
     if device_error is not None:
         _need("device_error", device_error, torch.int32, (1,), dev, index)
         err = device_error.data_ptr()
     if T > 0:
+        tok = N.Q8Tokens(k_new.data_ptr(), v_new.data_ptr(), q_ptr, q_out_ptr, k_stride, v_stride,
+                         q_stride, cs_ptr, cu_ptr, T, n_pos, rot, 1 if interleaved else 0)
         _q8_launch("lychee_append_rope_q8", N.load().lychee_append_rope_q8, dev, index, stream,
                    (sh, ptrs, tok, seqlens.data_ptr(), err))
     return q_out

@@ -423,6 +423,64 @@ def test_streams_and_repeatability():
         assert torch.equal(hyb[0], hyb2[0]) and torch.equal(hyb[1], hyb2[1])
 
 
+def test_rotated_queries_in_place():
+    """q_out may be q itself."""
+    g = torch.Generator().manual_seed(31)
+    seq = torch.tensor([9, 40], dtype=torch.int32)
+    cache = to_dev(R.make_cache(g, 8, 2, 16, 128, E4))
+    table = torch.arange(8, dtype=torch.int32).view(2, 4)
+    q, kn = torch.randn(2, 8, 128, generator=g).to(BF).to(DEV), torch.randn(2, 2, 128, generator=g).to(BF).to(DEV)
+    cs = cos_sin(64, 96).to(DEV)
+    apart = ops.append_rope_q8(kn, kn, cache, table.to(DEV), seq.to(DEV), cs, q=q)
+    same_place = q.clone()
+    assert ops.append_rope_q8(kn, kn, cache, table.to(DEV), seq.to(DEV), cs, q=same_place, q_out=same_place) is same_place
+    torch.cuda.synchronize()
+    assert same(apart, same_place)
+
+
+def test_calls_back_to_back_in_one_workspace():
+    """Calls of different shapes queued one behind another in one workspace, the launches overlapping
+    as they may, give what each gives alone."""
+    jobs = []
+    for seed, lens, roles, share in ((1, [9000], [1] + [0] * 7, 0.3), (2, [4000, 800, 3], [0] * 8, 0.1),
+                                     (3, [2500, 2500], [1] * 8, 0.2), (4, [70 + i for i in range(40)], [1, 0, 0, 0, 0, 0, 0, 1], 0.3),
+                                     (5, [600], [0, 0, 1, 0, 0, 0, 0, 0], 0.3)):
+        g = torch.Generator().manual_seed(seed)
+        table, P = R.make_table(g, lens, 64)
+        cache = to_dev(R.make_cache(g, P, 2, 64, 128, E4))
+        k = max(1, int(max(lens) * share))
+        idx = torch.full((len(lens), 8, k), -1, dtype=torch.int32)
+        for b, n in enumerate(lens):
+            m = max(1, int(n * share))
+            idx[b, :, :m] = torch.rand(8, n, generator=g).topk(m, dim=1).indices.sort(dim=1).values.int()
+        rows = torch.randn(len(lens), 2, 128, generator=g).to(BF).to(DEV)
+        jobs.append((torch.randn(len(lens), 8, 128, generator=g).to(BF).to(DEV), cache, table.to(DEV),
+                     torch.tensor(lens, dtype=torch.int32, device=DEV), roles, idx.to(DEV), k, rows, P))
+    n = max(ops.q8_workspace_size(q.shape[0], 8, 2, 128, 64, P, t.shape[1], BF, E4, k) for q, _, t, _, _, _, k, _, P in jobs)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+
+    def run(job):
+        q, cache, table, seq, roles, idx, k, rows, _ = job
+        ops.append_rope_q8(rows, rows, cache, table, seq)     # (the same rows again: nothing changes)
+        kps = (seq.float() * 0.3).int().clamp(min=1)
+        return (ops.decode_attn_q8(q, cache, table, seq, workspace=ws),
+                *ops.hybrid_decode_attn_q8(q, cache, table, seq, roles, idx, k, k_per_seq=kps, workspace=ws))
+
+    for job in jobs:
+        run(job)
+    alone = []
+    for job in jobs:
+        torch.cuda.synchronize()
+        alone.append([x.clone() for x in run(job)])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        order = [0, 3, 1, 4, 2, 0, 2, 4, 1, 3]
+        outs = [run(jobs[i]) for i in order]
+        torch.cuda.synchronize()
+        for i, got in zip(order, outs):
+            assert all(torch.equal(a, b) for a, b in zip(got, alone[i]))
+
+
 def test_a_decode_step_captured_and_replayed():
     """A prompt, then tokens one by one, as a serving loop runs them: the step (append with rotation,
     attention, hybrid layer) is captured once and replayed with lengths and rows changed in place;
