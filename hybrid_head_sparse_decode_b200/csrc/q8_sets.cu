@@ -30,7 +30,7 @@ constexpr int kSamples = 4;                   // samples a thread takes in a sea
 constexpr int kFan = 64 * kSamples;           // ... and a search (two warps) at once
 constexpr int kSearches = kThreads / 64;
 constexpr int kCopyRow = 16 * kThreads;       // entries a copying CTA takes
-constexpr int kBatch = 8;                     // consecutive entries a thread takes at once
+constexpr int kBatch = 12;                    // consecutive entries a thread takes at once (sets of 30 %: one round)
 
 // One tile.  The set of sparse head t of the group: entries [from, to) of its row
 // lie in the tile.

@@ -36,7 +36,8 @@ BAD = [(dict(B=0), N.ERR_INVALID_ARG), (dict(Hkv=0), N.ERR_INVALID_ARG), (dict(p
        (dict(Hq=32), N.ERR_UNSUPPORTED), (dict(Hq=256, Hkv=64), N.ERR_UNSUPPORTED), (dict(d=96), N.ERR_UNSUPPORTED),
        (dict(d=256), N.ERR_UNSUPPORTED), (dict(page=8), N.ERR_UNSUPPORTED), (dict(page=48), N.ERR_UNSUPPORTED),
        (dict(page=256), N.ERR_UNSUPPORTED), (dict(max_pages=(1 << 18) + 1), N.ERR_UNSUPPORTED),
-       (dict(num_pages=1 << 24), N.ERR_UNSUPPORTED), (dict(B=1 << 22), N.ERR_UNSUPPORTED)]
+       (dict(num_pages=1 << 24), N.ERR_UNSUPPORTED), (dict(B=1 << 22), N.ERR_UNSUPPORTED),
+       (dict(B=1 << 17, max_pages=1 << 18), N.ERR_UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("change,status", BAD)
