@@ -49,7 +49,7 @@
 // transpose of 8x8 halves (movmatrix).
 //
 // Bound by memory where there is enough to read: 131072 positions of 8 KV heads of
-// 128 (268 MB) take 48.8 us, of which the slabs 38 (7.1 TB/s), finding the ranges and
+// 128 (268 MB) take 49 us, of which the slabs 38 (7.1 TB/s), finding the ranges and
 // the first rows 5, merging and the second launch 5.  Next to it stand the
 // instructions (a 16-row step took 415 of them in slabs of 16, and less in slabs of
 // 32, whose bookkeeping is shared): int8 codes, two more per pair to become halves,
@@ -920,7 +920,18 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     uint32_t phase = 0;
     for (int i = 0; i < copied; ++i) {
       uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX) + si;
-      if (!mbar_wait(bar, phase, p.err)) break;   // (flagged; the result is lost)
+      if (!mbar_wait(bar, phase, p.err)) {
+        // flagged, and the result is lost; what is still on its way gets as long again
+        for (; i < copied; ++i) {
+          mbar_wait(bar, phase, p.err);
+          if (++si == kStages) {
+            si = 0;
+            phase ^= 1u;
+          }
+          bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX) + si;
+        }
+        break;
+      }
       __syncwarp();
       const uint2 hd = lds64(wk.aux + si * C::AUX + C::AUX_HEAD);
       if ((int)hd.x != seg) {
