@@ -20,8 +20,8 @@
 // reference is kept 6 below the maximum seen and moved only when a weight would
 // pass 2^15: weights down to 2^-31 of the largest keep a place in the half's range
 // (an 8-bit float's range would lose the many small weights of a long context).
-// With bf16 queries a weight is rounded to 11 bits (the output has 8); with fp32
-// ones it is held in two halves.
+// A weight is held in two halves (22 bits): one alone (11 bits) moves every tenth
+// bf16 output to its neighbour.
 //
 // Work split.  The unit is a slab of 32 rows of one KV head.  All slabs of the
 // call, ordered by sequence, head and position, are cut into one equal range per
@@ -165,9 +165,11 @@ __device__ __forceinline__ void store4(float* p, float a, float b, float c, floa
 
 template <typename T, int CODE, int D, int G>
 struct Cfg {
-  static constexpr bool kTwo = sizeof(T) == 4;           // q and the weights in two halves
-  static constexpr bool kBeside = kTwo && G <= 4;        // ... in columns 0-3 and 4-7 of one product
-  static constexpr int NQ = kTwo && !kBeside ? 2 : 1;    // ... or in two products
+  static constexpr bool kTwoQ = sizeof(T) == 4;          // q in two halves (the weights always are)
+  static constexpr bool kBeside = G <= 4;                // ... in columns 0-3 and 4-7 of one product (a q of
+                                                         // one half stands in both)
+  static constexpr int NQ = kTwoQ && !kBeside ? 2 : 1;   // ... or in two products
+  static constexpr int NP = kBeside ? 1 : 2;
   static constexpr int KM = D / 16;                      // blocks of 16 dimensions of O
   static constexpr int H = D / 64;                       // 16-byte pieces of K a lane takes of a row
   static constexpr int VB = D / 8;                       // bytes of V a lane takes of each of its four rows
@@ -467,7 +469,7 @@ struct Warp {
     for (int m = 0; m < C::KM; ++m) {
       const float a = x[m].x * up, bb = x[m].y * up, cc = x[m].z * up, d = x[m].w * up;
       uint32_t w0 = pack_half(a, bb), w1 = pack_half(cc, d);
-      if constexpr (C::kTwo) {
+      if constexpr (C::kTwoQ) {
         const float2 h0 = unpack_half(w0), h1 = unpack_half(w1);
         const uint32_t l0 = pack_half(a - h0.x, bb - h0.y), l1 = pack_half(cc - h1.x, d - h1.y);
         if constexpr (C::NQ == 2) {
@@ -518,7 +520,7 @@ struct Warp {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[a][i] += s2[i];
-      if (C::kBeside) {
+      if (C::kTwoQ && C::kBeside) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[a][i] += __shfl_xor_sync(kFull, s[a][i], 2);
       }
@@ -600,7 +602,7 @@ struct Warp {
       }
     }
     // weights, their sums without the scales, and the weights as B
-    uint32_t pb[2][C::kTwo && !C::kBeside ? 2 : 1][2];
+    uint32_t pb[2][C::NP][2];
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -612,12 +614,10 @@ struct Warp {
           l[j] = fmaf(w[j], inv[a][i], l[j]);
         }
         uint32_t hi = pack_half(w[0], w[1]);
-        if constexpr (C::kTwo) {
-          const float2 hf = unpack_half(hi);
-          const uint32_t lo = pack_half(w[0] - hf.x, w[1] - hf.y);
-          if constexpr (!C::kBeside) pb[a][1][i] = movmatrix_trans(lo);
-          else if (c >= 2) hi = lo;
-        }
+        const float2 hf = unpack_half(hi);
+        const uint32_t lo = pack_half(w[0] - hf.x, w[1] - hf.y);
+        if constexpr (C::NP == 2) pb[a][1][i] = movmatrix_trans(lo);
+        else if (c >= 2) hi = lo;
         pb[a][0][i] = movmatrix_trans(hi);
       }
     // ---- O: k indices 2c, 2c + 1, 2c + 8, 2c + 9 of a half are rows Ra, Rb, Ra + 8, Rb + 8
@@ -644,7 +644,7 @@ struct Warp {
           codes_to_half<CODE>(__byte_perm(v[0][k], v[1][k], sel), a0, a1);
           codes_to_half<CODE>(__byte_perm(v[2][k], v[3][k], sel), a2, a3);
           mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[a][0][0], pb[a][0][1]);
-          if constexpr (C::kTwo && !C::kBeside) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[a][1][0], pb[a][1][1]);
+          if constexpr (C::NP == 2) mma_f16(acc[2 * k + half], a0, a1, a2, a3, pb[a][1][0], pb[a][1][1]);
         }
       }
     }

@@ -410,8 +410,8 @@ LYCHEE_API size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k);
  *   workspace device, >= lychee_q8_workspace_size(s, 0) bytes, 256-byte aligned
  * Scores are exact products of the codes with q (bf16, down to 2^-27 of its largest
  * element), or with q held in two 11-bit parts (fp32), summed in fp32; softmax and
- * sums are fp32; the softmax weights (times the V scale) are rounded to 11 bits
- * (bf16) or held in two such parts (fp32), and to 2^-31 of a head's largest. */
+ * sums are fp32; the softmax weights (times the V scale) are held in two 11-bit
+ * parts, and to 2^-31 of a head's largest. */
 LYCHEE_API lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q,
                                                const lychee_q8_cache* cache, const int32_t* seqlens,
                                                void* out, void* workspace, size_t workspace_bytes,
