@@ -235,12 +235,11 @@ __global__ void __launch_bounds__(kSelThreads, D >= 128 ? 2 : 1)
   static_assert(kSelThreads == kCombThreads, "one block size for both roles");
   extern __shared__ __align__(16) uint32_t dsm[];
   unsigned char* csm = reinterpret_cast<unsigned char*>(dsm);
-  if (!p.trigger_late) pdl_launch_dependents();
+  pdl_launch_dependents();
   const int cta = blockIdx.x;
   if (cta < nsel) block_select_prologue(dsm);
   else combine_prologue<D>(csm);
   pdl_wait();
-  if (p.trigger_late) pdl_launch_dependents();
   if (cta < nsel) block_select_body(p, cta / kSelCtas, dsm);
   else combine_body<T, D>(cp, cta - nsel, csm);
 }

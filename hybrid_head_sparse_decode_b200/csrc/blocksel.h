@@ -18,7 +18,6 @@ struct BlockSelParams {
   uint32_t* err;
   int B, Hq, N_max, nwords, k, nheads, block;
   int empty_ok;              // 1: a sequence of no rows gets an empty set (0: n_b counts as 1)
-  int trigger_late;          // as TopkParams::trigger_late
   uint8_t heads[128];        // the retrieval heads handled by this launch
 };
 // block keys of one head, at most 32768 blocks (see block_select_smem)

@@ -87,8 +87,6 @@ struct TopkParams {
   int sms;                   // SMs of the device (the cluster size is picked by waves)
   int empty_ok;              // 1: a sequence of no rows gets an empty set (0: n_b counts as 1)
   int alone;                 // 1: no attention kernel runs beside the selection
-  int trigger_late;          // 1: the next kernel may start once the previous one is complete (it need
-                             // not wait for the selection before it reads what came earlier)
   uint8_t heads[128];        // the retrieval heads handled by this launch
 };
 

@@ -74,8 +74,7 @@ struct Q8AttnParams {
 cudaError_t launch_q8_sets(const Q8AttnParams& p, int dtype, int D, cudaStream_t st);
 cudaError_t launch_q8_attn(const Q8AttnParams& p, int dtype, int code, int D, int sms,
                            cudaStream_t st);
-// The states it left open.  beside: the launch before this one is a selection that
-// triggered late; the two then run side by side.
-cudaError_t launch_q8_merge(const Q8AttnParams& p, int dtype, int D, int sms, bool beside, cudaStream_t st);
+// The states it left open.
+cudaError_t launch_q8_merge(const Q8AttnParams& p, int dtype, int D, int sms, cudaStream_t st);
 
 }  // namespace lychee

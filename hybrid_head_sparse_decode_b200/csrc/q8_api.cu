@@ -210,7 +210,7 @@ lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q, con
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); });
   if (e == cudaSuccess)
-    e = timed(kKindCombine, cs, [&] { return launch_q8_merge(p, s->dtype, s->d, sms, false, cs); });
+    e = timed(kKindCombine, cs, [&] { return launch_q8_merge(p, s->dtype, s->d, sms, cs); });
   return e == cudaSuccess ? LYCHEE_OK : LYCHEE_ERR_CUDA;
 }
 
@@ -254,9 +254,11 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
     return LYCHEE_ERR_CUDA;
   if (timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); }) != cudaSuccess)
     return LYCHEE_ERR_CUDA;
-  if (ns == s->Hq)
-    return timed(kKindCombine, cs, [&] { return launch_q8_merge(p, s->dtype, s->d, sms, false, cs); }) == cudaSuccess
-               ? LYCHEE_OK : LYCHEE_ERR_CUDA;
+  // (merge and selection need the attention only, but a kernel sees what an earlier one
+  // wrote behind its own wait alone, and that is for the kernel before it)
+  if (timed(kKindCombine, cs, [&] { return launch_q8_merge(p, s->dtype, s->d, sms, cs); }) != cudaSuccess)
+    return LYCHEE_ERR_CUDA;
+  if (ns == s->Hq) return LYCHEE_OK;
   // the retrieval heads' selection, as over any cache
   TopkParams tp{};
   tp.logits = p.logits;
@@ -267,7 +269,6 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   tp.B = s->B; tp.Hq = s->Hq; tp.N_max = p.N_max; tp.nwords = L.nwords; tp.k = k;
   tp.sms = sms;
   tp.empty_ok = 1;
-  tp.trigger_late = 1;
   tp.alone = 1;
   for (int h = 0; h < s->Hq; ++h)
     if (head_role[h] == LYCHEE_ROLE_RETRIEVAL) tp.heads[tp.nheads++] = (uint8_t)h;
@@ -284,14 +285,11 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
     bp.nheads = tp.nheads;
     bp.block = block;
     bp.empty_ok = 1;
-    bp.trigger_late = 1;
     std::memcpy(bp.heads, tp.heads, sizeof(bp.heads));
     e = timed(kKindTopk, cs, [&] { return launch_block_select_combine(bp, none, s->dtype, s->d, cs); });
   } else {
     e = timed(kKindTopk, cs, [&] { return launch_topk_combine(tp, none, s->dtype, s->d, cs); });
   }
-  if (e != cudaSuccess) return LYCHEE_ERR_CUDA;
-  e = timed(kKindCombine, cs, [&] { return launch_q8_merge(p, s->dtype, s->d, sms, true, cs); });
   return e == cudaSuccess ? LYCHEE_OK : LYCHEE_ERR_CUDA;
 }
 

@@ -1098,20 +1098,15 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
 constexpr int kMergeThreads = 256;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8AttnParams p, int beside) {
+__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8AttnParams p) {
   constexpr int LPS = D / 4;                 // lanes a state
   constexpr int kGroups = kMergeThreads / LPS;
   __shared__ float s_acc[kGroups][D], s_m[kGroups], s_l[kGroups];
   pdl_launch_dependents();
-  // Behind a selection (beside) the launch itself came after the attention kernel
-  // had completed; the selection only has to be complete before this kernel is.
-  if (!beside) pdl_wait();
+  pdl_wait();
   const int first = blockIdx.x, h = blockIdx.y, ctas = gridDim.x, G = gridDim.y;
   const int seg = p.part_seg[2 * first + 1];
-  if (seg < 0) {
-    if (beside) pdl_wait();
-    return;
-  }
+  if (seg < 0) return;
   int more = 0;
   for (int i0 = first + 1; i0 < ctas; i0 += kMergeThreads) {
     const int i = i0 + threadIdx.x;
@@ -1148,7 +1143,6 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     const int b = seg / p.Hkv, g = seg - b * p.Hkv;
     store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + threadIdx.x, t.l > 0.f ? t.a / t.l : 0.f);
   }
-  if (beside) pdl_wait();
 }
 
 // ---- launches ----
@@ -1195,18 +1189,17 @@ cudaError_t launch_c(const Q8AttnParams& p, int D, int grid, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_q8_merge(const Q8AttnParams& p, int dtype, int D, int sms, bool beside, cudaStream_t st) {
+cudaError_t launch_q8_merge(const Q8AttnParams& p, int dtype, int D, int sms, cudaStream_t st) {
   const int grid = attn_grid(sms);
   if (takes_whole(p, grid)) return cudaSuccess;
   const dim3 g(grid, p.Hq / p.Hkv), b(kMergeThreads);
-  const int w = beside ? 1 : 0;
   cudaError_t e;
   if (dtype == 0)
-    e = D == 128 ? launch_pdl(q8_merge_kernel<__nv_bfloat16, 128>, g, b, 0, st, p, w)
-                 : launch_pdl(q8_merge_kernel<__nv_bfloat16, 64>, g, b, 0, st, p, w);
+    e = D == 128 ? launch_pdl(q8_merge_kernel<__nv_bfloat16, 128>, g, b, 0, st, p)
+                 : launch_pdl(q8_merge_kernel<__nv_bfloat16, 64>, g, b, 0, st, p);
   else
-    e = D == 128 ? launch_pdl(q8_merge_kernel<float, 128>, g, b, 0, st, p, w)
-                 : launch_pdl(q8_merge_kernel<float, 64>, g, b, 0, st, p, w);
+    e = D == 128 ? launch_pdl(q8_merge_kernel<float, 128>, g, b, 0, st, p)
+                 : launch_pdl(q8_merge_kernel<float, 64>, g, b, 0, st, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

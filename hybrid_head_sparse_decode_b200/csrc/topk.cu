@@ -340,14 +340,13 @@ __global__ void __launch_bounds__(kThreads, D >= 128 ? 2 : 1)
     topk_combine_kernel(const __grid_constant__ TopkParams p, const __grid_constant__ CombineParams cp,
                         int keys_cap, int wpc_cap, int ntopk, int ncomb) {
   extern __shared__ __align__(16) uint32_t dsm[];
-  if (!p.trigger_late) pdl_launch_dependents();
+  pdl_launch_dependents();
   static_assert(C % kCombineSplit == 0, "a head's combine CTAs share a cluster");
   const int cta = blockIdx.x;
   unsigned char* csm = reinterpret_cast<unsigned char*>(dsm);
   if (cta < ntopk) topk_prologue<C>(dsm);
   else combine_prologue<D>(csm);
   pdl_wait();
-  if (p.trigger_late) pdl_launch_dependents();
   if (cta < ntopk) topk_body<C>(p, keys_cap, wpc_cap, cta, dsm);
   else if (cta - ntopk < ncomb) combine_body<T, D>(cp, cta - ntopk, csm);
   else combine_idle();
