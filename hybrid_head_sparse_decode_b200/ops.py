@@ -9,9 +9,15 @@ Hybrid-Head Sparse Decoding" (paper.rainbus.top/paper/2602.04541), steps (1),
 only checks that tensors live on a CUDA device with the expected dtype and
 layout, allocates outputs/workspace with torch when the caller does not pass
 them, and hands raw pointers to the library on the current (or given) stream.
+
+With stream=, what a call allocates belongs to that stream: a workspace is reused
+behind the call's kernels only, and outputs are also kept until the stream that was
+current at the call is done with them.  Tensors that the caller passes have to be
+ready on the stream and kept until its kernels are done, as torch has it everywhere.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple
 
@@ -34,6 +40,21 @@ def _stream_handle(stream, device=None):
     if device is not None and s.device != device:
         raise ValueError(f"stream is on {s.device}, but the call runs on {device}")
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(stream):
+    """The context in which a call on `stream` (None: the current one) allocates."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty_out(shape, dtype, device, stream):
+    """An output of a call on `stream`, which the caller's stream may read after it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _need_cuda(name, t, dtype=None, shape=None, device=None):
@@ -133,14 +154,15 @@ def hybrid_decode_attn(q, k_cache, v_cache, seqlens, head_role, idx_in, k, *, k_
         _need_cuda("idx_in", idx_in, torch.int32, (B, Hq, k), device=dev)
     role = _roles_host(head_role, Hq)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=dt, device=q.device)
+        out = _empty_out((B, Hq, d), dt, q.device, stream)
     _need_cuda("out", out, dt, (B, Hq, d), device=dev)
     if idx_out is None:
-        idx_out = torch.empty((B, Hq, k), dtype=torch.int32, device=q.device)
+        idx_out = _empty_out((B, Hq, k), torch.int32, q.device, stream)
     _need_cuda("idx_out", idx_out, torch.int32, (B, Hq, k), device=dev)
     sh = make_shape(B, Hq, Hkv, d, N_max, k, dt, block)
     if workspace is None:
-        workspace = alloc_workspace(B, Hq, Hkv, d, N_max, k, dt, q.device, block)
+        with _on(stream):
+            workspace = alloc_workspace(B, Hq, Hkv, d, N_max, k, dt, q.device, block)
     _need_cuda("workspace", workspace, torch.uint8, device=dev)
     if swa is not None:
         window = _check_swa(swa, B, Hkv, d, dt, dev, (B, Hq))
@@ -188,10 +210,10 @@ def hybrid_decode_attn_noalloc(q, k_cache, v_cache, seqlens, head_role, idx_in, 
                          f"{N.NOALLOC_SCRATCH_BYTES} (use hybrid_decode_attn with a workspace)")
     role = _roles_host(head_role, Hq)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=dt, device=q.device)
+        out = _empty_out((B, Hq, d), dt, q.device, stream)
     _need_cuda("out", out, dt, (B, Hq, d), device=dev)
     if idx_out is None:
-        idx_out = torch.empty((B, Hq, k), dtype=torch.int32, device=q.device)
+        idx_out = _empty_out((B, Hq, k), torch.int32, q.device, stream)
     _need_cuda("idx_out", idx_out, torch.int32, (B, Hq, k), device=dev)
     if device_error is not None:
         _need_cuda("device_error", device_error, torch.int32, (1,), device=dev)
@@ -228,18 +250,19 @@ def decode_stack(q, k_caches, v_caches, seqlens, head_roles, k, *, k_per_seq=Non
         _need_cuda("k_per_seq", k_per_seq, torch.int32, (B,), device=dev)
     roles = _roles_host(head_roles, L * Hq)
     if out is None:
-        out = torch.empty((L, B, Hq, d), dtype=dt, device=q.device)
+        out = _empty_out((L, B, Hq, d), dt, q.device, stream)
     _need_cuda("out", out, dt, (L, B, Hq, d), device=dev)
     if idx_final is None:
-        idx_final = torch.empty((B, Hq, k), dtype=torch.int32, device=q.device)
+        idx_final = _empty_out((B, Hq, k), torch.int32, q.device, stream)
     _need_cuda("idx_final", idx_final, torch.int32, (B, Hq, k), device=dev)
     if idx_layers is None and want_layers:
-        idx_layers = torch.empty((L, B, Hq, k), dtype=torch.int32, device=q.device)
+        idx_layers = _empty_out((L, B, Hq, k), torch.int32, q.device, stream)
     if idx_layers is not None:
         _need_cuda("idx_layers", idx_layers, torch.int32, (L, B, Hq, k), device=dev)
     sh = make_shape(B, Hq, Hkv, d, N_max, k, dt, block)
     if workspace is None:
-        workspace = alloc_workspace(B, Hq, Hkv, d, N_max, k, dt, q.device, block)
+        with _on(stream):
+            workspace = alloc_workspace(B, Hq, Hkv, d, N_max, k, dt, q.device, block)
     _need_cuda("workspace", workspace, torch.uint8, device=dev)
     kp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in k_caches])
     vp = (ctypes.c_void_p * L)(*[t.data_ptr() for t in v_caches])
@@ -464,7 +487,7 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
         Hq = q.shape[1]
         q_stride = _need_rows("q", q, dt, (T, Hq, d), dev, index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+            q_out = _empty_out((T, Hq, d), dt, dev, stream)
         else:
             _need("q_out", q_out, dt, (T, Hq, d), dev, index)
         q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
@@ -497,7 +520,7 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
     return q_out
 
 
-def _q8_call(q, cache, block_table, seqlens, out, workspace, device_error, k):
+def _q8_call(q, cache, block_table, seqlens, out, workspace, device_error, k, stream):
     """What both attention calls check and make: (shape, pointers, B, Hq, device, its index, out,
     workspace, device_error's pointer)."""
     index = _device_index("q", q)
@@ -508,7 +531,7 @@ def _q8_call(q, cache, block_table, seqlens, out, workspace, device_error, k):
         raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
     _need("q", q, dt, shape, dev, index)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_out(shape, dt, dev, stream)
     else:
         _need("out", out, dt, shape, dev, index)
     sh, ptrs, B, _ = _q8_cache(cache, block_table, seqlens, shape[1], shape[2], dt, dev, index)
@@ -516,7 +539,8 @@ def _q8_call(q, cache, block_table, seqlens, out, workspace, device_error, k):
         raise ValueError(f"q has {shape[0]} sequences, block_table {B}")
     if workspace is None:
         n = N.load().lychee_q8_workspace_size(sh, k)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        with _on(stream):
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and
               workspace.get_device() == index and workspace.is_contiguous()):
         _need_cuda("workspace", workspace, torch.uint8, device=dev)
@@ -534,7 +558,7 @@ def decode_attn_q8(q, cache, block_table, seqlens, *, out=None, workspace=None, 
     workspace: uint8, q8_workspace_size(...) bytes (calls that share one must be ordered on one
     stream; None: a fresh one).  device_error as in append_rope_q8.  Returns out [B, Hq, d]."""
     sh, ptrs, _, _, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,
-                                                               workspace, device_error, 0)
+                                                               workspace, device_error, 0, stream)
     _q8_launch("lychee_decode_attn_q8", N.load().lychee_decode_attn_q8, dev, index, stream,
                (sh, q.data_ptr(), ptrs, seqlens.data_ptr(), out.data_ptr(), workspace.data_ptr(),
                 workspace.numel(), err))
@@ -550,7 +574,8 @@ def hybrid_decode_attn_q8(q, cache, block_table, seqlens, head_role, idx_in, k, 
     Returns (out [B, Hq, d], idx_out [B, Hq, k])."""
     k = int(k)
     sh, ptrs, B, Hq, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,
-                                                                workspace, device_error, max(k, 0))
+                                                                workspace, device_error, max(k, 0),
+                                                                stream)
     kps = idx = None
     if k_per_seq is not None:
         _need("k_per_seq", k_per_seq, torch.int32, (B,), dev, index)
@@ -563,7 +588,7 @@ def hybrid_decode_attn_q8(q, cache, block_table, seqlens, head_role, idx_in, k, 
             not role.is_cuda and role.is_contiguous()):
         role = _roles_host(head_role, Hq)
     if idx_out is None:
-        idx_out = torch.empty((B, Hq, max(k, 0)), dtype=torch.int32, device=dev)
+        idx_out = _empty_out((B, Hq, max(k, 0)), torch.int32, dev, stream)
     else:
         _need("idx_out", idx_out, torch.int32, (B, Hq, k), dev, index)
     _q8_launch("lychee_hybrid_decode_attn_q8", N.load().lychee_hybrid_decode_attn_q8, dev, index,
@@ -584,9 +609,9 @@ def hardkuma_roles(alpha, beta, p=-0.1, q=1.1, layer0_retrieval=True, stream=Non
         raise ValueError("alpha must be [L, Hq]")
     L, Hq = alpha.shape
     _need_cuda("beta", beta, torch.float64, (L, Hq), device=dev)
-    roles = torch.empty((L, Hq), dtype=torch.uint8, device=dev)
-    ez = torch.empty((L, Hq), dtype=torch.float64, device=dev)
-    l0 = torch.empty((1,), dtype=torch.float64, device=dev)
+    roles = _empty_out((L, Hq), torch.uint8, dev, stream)
+    ez = _empty_out((L, Hq), torch.float64, dev, stream)
+    l0 = _empty_out((1,), torch.float64, dev, stream)
     with torch.cuda.device(dev):
         st = N.load().lychee_hardkuma_roles(_ptr(alpha), _ptr(beta), int(L), int(Hq), float(p),
                                             float(q), int(bool(layer0_retrieval)), _ptr(roles),
