@@ -376,6 +376,12 @@ struct Warp {
       const bool in = lane < rest && ((oks >> (lane >> 4)) & 1u);
       myrow = in ? (lane < 16 ? half0 : half1) + (lane & 15) : kAbsent;
       heads = __ballot_sync(kFull, in) & (HYB && mixed ? pre_m : 0xffffffffu);
+      if (HYB && lane < rest && !in) {
+        // a position without a page ranks last in the sets that are handed on
+#pragma unroll 1
+        for (int t = 0; t < G; ++t)
+          if (retrieval(g * G + t)) p.logits[((size_t)seg * G + t) * p.N_max + pos0 + lane] = -INFINITY;
+      }
     } else {
       myrow = pre;
       heads = 0;

@@ -331,7 +331,9 @@ LYCHEE_API lychee_status lychee_hardkuma_roles(const double* alpha, const double
  *     bad sequence length; 16 = the append met a value that is not finite).  It
  *     is never cleared here: the caller sets it to zero and reads it when it
  *     likes.
- *   - A page number outside [0, num_pages) is flagged and its rows are skipped.
+ *   - A page number outside [0, num_pages) is flagged and its rows are skipped:
+ *     no head attends to them, and in the sets that retrieval heads hand on they
+ *     rank last (by lower position), behind every row that there is.
  */
 typedef enum { LYCHEE_E4M3 = 0, LYCHEE_INT8 = 1 } lychee_code;
 

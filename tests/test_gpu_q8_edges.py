@@ -1,0 +1,77 @@
+"""The 8-bit cache's calls at the edges of what their documentation allows: bad pages, queries and scores that are not
+ordinary numbers, workspaces that held something else."""
+import pytest
+import torch
+
+import q8_ref as R
+from hybrid_head_sparse_decode_b200 import _native as N
+from hybrid_head_sparse_decode_b200 import ops
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E4, I8 = torch.float8_e4m3fn, torch.int8
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def to_dev(cache):
+    return ops.Q8Cache(*(t.to(DEV) for t in cache))
+
+
+# ---- pages that are none --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,code,page,n,block", [(BF, E4, 64, 1500, 0), (F32, I8, 16, 300, 0), (BF, I8, 32, 9000, 64),
+                                                     (BF, E4, 16, 1030, 32)])
+def test_positions_on_bad_pages_rank_last(dtype, code, page, n, block):
+    """A retrieval head's set holds no position whose page is none while there are others, whatever the workspace held; and
+    no head attends to one."""
+    g = torch.Generator().manual_seed(17)
+    lens, Hq, Hkv, d = [n, 90], 16, 4, 64
+    roles = [1, 0, 0, 0] + [1, 1, 1, 1] + [0, 0, 0, 0] + [0, 0, 1, 1]
+    table, P = R.make_table(g, lens, page)
+    cache = R.make_cache(g, P, Hkv, page, d, code)
+    q = torch.randn(2, Hq, d, generator=g).to(dtype)
+    bad = table.clone()
+    last = (n + page - 1) // page - 1
+    for j, x in ((0, -1), (last // 2, P), (last // 2 + 1, 1 << 30), (last, -7)):
+        bad[0, j] = x
+    here = [torch.tensor([0 <= int(bad[b, i // page]) < P for i in range(m)]) for b, m in enumerate(lens)]
+    k = 256
+    sets = [[None if roles[h] else torch.nonzero(torch.rand(lens[b], generator=g) < 0.1)[:k, 0] for h in range(Hq)] for b in range(2)]
+    idx = torch.full((2, Hq, k), -1, dtype=torch.int32)
+    for b in range(2):
+        for h in range(Hq):
+            if sets[b][h] is not None:
+                idx[b, h, :len(sets[b][h])] = sets[b][h].int()
+    keep = [[(torch.nonzero(here[b])[:, 0] if s is None else s[here[b][s]]) for s in sets[b]] for b in range(2)]
+    seq = torch.tensor(lens, dtype=torch.int32)
+    ref, tol, raws, rts = R.attend(q, cache, torch.where((bad < 0) | (bad >= P), 0, bad), seq, keep)
+    size = ops.q8_workspace_size(2, Hq, Hkv, d, page, P, table.shape[1], dtype, code, k)
+    seen = []
+    for fill in (0, 0x7f, 0xff):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out, nxt = ops.hybrid_decode_attn_q8(q.to(DEV), to_dev(cache), bad.to(DEV), seq.to(DEV), roles, idx.to(DEV), k,
+                                             workspace=ws, device_error=err, block=block)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 1
+        off = (out.cpu().double() - ref).abs()
+        assert bool((off <= tol + 1e-30).all())
+        nxt = nxt.cpu()
+        seen.append(nxt)
+        for b in range(2):
+            for h in range(Hq):
+                if not roles[h]:
+                    assert torch.equal(nxt[b, h], idx[b, h])
+                    continue
+                got = nxt[b, h][nxt[b, h] >= 0].long()
+                raw = torch.where(here[b], raws[b][h], -torch.inf)
+                if block:
+                    nblk = (lens[b] + block - 1) // block
+                    score = torch.stack([raw[i * block:(i + 1) * block].max() for i in range(nblk)])
+                    R.check_topk(torch.unique(got // block), score, min(max(1, min(k, lens[b]) // block), nblk), float(rts[b][h]))
+                else:
+                    R.check_topk(got, raw, min(k, lens[b]), float(rts[b][h]))
+                    # (the rest of a set larger than what is there: the lowest positions)
+                    lost = got[~here[b][got]]
+                    assert torch.equal(lost, torch.nonzero(~here[b])[:len(lost), 0])
+    assert torch.equal(seen[0], seen[1]) and torch.equal(seen[0], seen[2])
