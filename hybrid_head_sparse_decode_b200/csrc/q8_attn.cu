@@ -676,7 +676,7 @@ struct Warp {
     for (int j = 0; j < 2; ++j) {
       const int h = column_head(j);
       if (h >= G || (C::kBeside && c >= 2)) continue;
-      const float inv = l[j] > 0.f ? 1.f / l[j] : 0.f;
+      const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];   // (a NaN stays one)
       T* o = static_cast<T*>(p.out) + ((size_t)sg * G + h) * D + r * C::VB;
 #pragma unroll
       for (int m = 0; m < C::KM; ++m) {
@@ -1078,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     const float L = s_l[h][e0];
     if (out) {
       const int b = cseg / p.Hkv, g = cseg - b * p.Hkv;
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
       store4(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + e, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     } else {
       float* s = p.parts + ((size_t)blockIdx.x * 2 + slot) * C::STATE;
@@ -1147,7 +1147,7 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     t.clear();
     for (int i = 0; i < kGroups; ++i) t.add(s_m[i], s_l[i], s_acc[i][threadIdx.x]);
     const int b = seg / p.Hkv, g = seg - b * p.Hkv;
-    store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + threadIdx.x, t.l > 0.f ? t.a / t.l : 0.f);
+    store1(static_cast<T*>(p.out) + ((size_t)b * p.Hq + g * G + h) * D + threadIdx.x, t.l == 0.f ? 0.f : t.a / t.l);
   }
 }
 

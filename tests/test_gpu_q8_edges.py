@@ -75,3 +75,35 @@ def test_positions_on_bad_pages_rank_last(dtype, code, page, n, block):
                     lost = got[~here[b][got]]
                     assert torch.equal(lost, torch.nonzero(~here[b])[:len(lost), 0])
     assert torch.equal(seen[0], seen[1]) and torch.equal(seen[0], seen[2])
+
+
+# ---- queries and scores that are not ordinary numbers ---------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 300, 1030, 20000])
+@pytest.mark.parametrize("dtype,Hq", [(BF, 8), (F32, 8), (BF, 16), (F32, 2)])
+def test_queries_that_are_no_numbers(dtype, Hq, n):
+    """A NaN or an infinity in a query makes its head's output NaN, however the work is split; the other heads' are as
+    without it.  A head whose set is empty gives zeros all the same."""
+    g = torch.Generator().manual_seed(23)
+    Hkv, d, page = 2, 128, 64
+    table, P = R.make_table(g, [n], page)
+    cache = to_dev(R.make_cache(g, P, Hkv, page, d, E4))
+    table, seq = table.to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = torch.randn(1, Hq, d, generator=g).to(dtype).to(DEV)
+    bad = q.clone()
+    bad[0, 0, 77] = float("nan")
+    bad[0, Hq - 1, 0] = -float("inf")
+    hit = torch.zeros(Hq, dtype=torch.bool, device=DEV)
+    hit[0] = hit[Hq - 1] = True
+    out, want = ops.decode_attn_q8(bad, cache, table, seq), ops.decode_attn_q8(q, cache, table, seq)
+    assert bool(out[0, hit].isnan().all()) and torch.equal(out[0, ~hit], want[0, ~hit])
+    k = min(n, 50)
+    idx = torch.arange(k, dtype=torch.int32, device=DEV).expand(1, Hq, k).contiguous()
+    for roles in ([1] * Hq, [0] * Hq, [1] + [0] * (Hq - 1)):
+        got, sets = ops.hybrid_decode_attn_q8(bad, cache, table, seq, roles, idx, k)
+        want, _ = ops.hybrid_decode_attn_q8(q, cache, table, seq, roles, idx, k)
+        assert bool(got[0, hit].isnan().all()) and torch.equal(got[0, ~hit], want[0, ~hit])
+        assert bool((sets[0, :, 1:] > sets[0, :, :-1]).all()) and int(sets.min()) >= 0 and int(sets.max()) < n
+    none = torch.full_like(idx, -1)
+    got, _ = ops.hybrid_decode_attn_q8(bad, cache, table, seq, [0] * Hq, none, k)
+    assert not bool(got.any())
