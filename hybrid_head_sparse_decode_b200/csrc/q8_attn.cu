@@ -74,7 +74,7 @@ constexpr int kSegCost = 1;
 constexpr float kRefBelow = 6.f;     // the reference lies this far below the maximum (log2)
 constexpr float kRefSlack = 15.f;    // and moves when a weight passes it by more than this
 constexpr uint32_t kAbsent = 0xffffffffu;  // of a slab's rows: none
-constexpr float kNoRef = -1e30f;     // no row yet (finite: differences of two stay numbers)
+constexpr float kNoRef = -3.402823466e38f;   // no row yet: the lowest finite number (differences of two stay numbers)
 constexpr uint32_t kFullSlab = 1u << 29;   // stage header: consecutive rows, a scale a half
 constexpr uint32_t kAllHeads = 1u << 30;   // ... and every head uses every row
 
@@ -568,7 +568,7 @@ struct Warp {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          s[a][2 * i + j] *= sk[a][i] * fq[j];
+          s[a][2 * i + j] = s[a][2 * i + j] * sk[a][i] * fq[j];   // (the scale first: the two factors' product may overflow)
           const bool on = (used[j] >> (16 * a + 8 * i)) & 1u;
           t[a][2 * i + j] = on ? fmaf(s[a][2 * i + j], p.scale_log2, lv[a][i]) : -INFINITY;
           top[j] = fmaxf(top[j], t[a][2 * i + j]);

@@ -414,7 +414,8 @@ LYCHEE_API size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k);
  * element), or with q held in two 11-bit parts (fp32), summed in fp32; softmax and
  * sums are fp32; the softmax weights (times the V scale) are held in two 11-bit
  * parts, and to 2^-31 of a head's largest.  A query that holds a NaN or an infinity
- * makes its head's output NaN (unless there is no row). */
+ * makes its head's output NaN (unless there is no row).  A dot product past fp32's
+ * range counts as an infinity: +, the output is NaN; -, the row has no weight. */
 LYCHEE_API lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q,
                                                const lychee_q8_cache* cache, const int32_t* seqlens,
                                                void* out, void* workspace, size_t workspace_bytes,

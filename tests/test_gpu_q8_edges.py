@@ -107,3 +107,37 @@ def test_queries_that_are_no_numbers(dtype, Hq, n):
     none = torch.full_like(idx, -1)
     got, _ = ops.hybrid_decode_attn_q8(bad, cache, table, seq, [0] * Hq, none, k)
     assert not bool(got.any())
+
+
+@pytest.mark.parametrize("n", [40, 5000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scores_near_the_end_of_fp32(dtype, n):
+    """Scores of -1e34, all equal or with one above the rest, and huge queries on rows of zeros: softmaxes like any other."""
+    g = torch.Generator().manual_seed(29)
+    Hq, Hkv, d, page = 8, 2, 128, 32
+    table, P = R.make_table(g, [n], page)
+    cache = R.make_cache(g, P, Hkv, page, d, I8)
+    seq = torch.tensor([n], dtype=torch.int32)
+    cache[2].fill_(1.0)
+    cache[0].fill_(-1)
+    q = torch.full((1, Hq, d), 2.0 ** 106, dtype=dtype)
+    idx = torch.arange(n, dtype=torch.int32).expand(1, Hq, n).contiguous()
+
+    def check():
+        ref, tol, _, _ = R.attend(q, cache, table, seq)
+        args = q.to(DEV), to_dev(cache), table.to(DEV), seq.to(DEV)
+        for out in (ops.decode_attn_q8(*args), ops.hybrid_decode_attn_q8(*args, [0] * Hq, idx.to(DEV), n)[0]):
+            off = (out.cpu().double() - ref).abs()
+            # (the scores are powers of two or zeros, exact in every step: nothing is lost in them)
+            V = R.rows_of(cache[1], cache[3], table[0], n)
+            assert bool((off <= 2.0 ** -8 * ref.abs() + 2.0 ** -16 * V.abs().max()).all()), float(off.max())
+
+    check()                                         # the mean of the values
+    at = n // 3
+    cache[0][int(table[0, at // page]), :, at % page] = -127
+    cache[0][int(table[0, 0]), :, 1] = 0            # one row's scores are 0, above all others
+    check()
+    cache[0].fill_(0)                               # scores of 0 with the largest query and scale
+    cache[2].fill_(2.0 ** 60)
+    q.fill_(2.0 ** 127)
+    check()
