@@ -19,6 +19,12 @@ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether na bytes at a and nb bytes at b share any.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 inline lychee_status check_roles(const uint8_t* role, int Hq, int* n_sparse) {
   if (!role) return LYCHEE_ERR_INVALID_ARG;
   int ns = 0;

@@ -60,6 +60,11 @@ Q8Cache cache_of(const lychee_q8_shape* s, const lychee_q8_cache* c) {
 
 int n_max_of(const lychee_q8_shape* s) { return s->max_pages * s->page; }
 
+// Bytes of q, and of out.
+size_t rows_bytes(const lychee_q8_shape* s) {
+  return (size_t)s->B * s->Hq * s->d * (s->dtype == LYCHEE_BF16 ? 2 : 4);
+}
+
 // Workspace: the states that the attention CTAs leave open; for the hybrid step
 // (k > 0) also the retrieval heads' logits and the sparse heads' sets as bitmaps
 // and row lists.
@@ -167,6 +172,18 @@ lychee_status lychee_append_rope_q8(const lychee_q8_shape* s, const lychee_q8_ca
   if (t->cos_sin && (t->rot < 8 || t->rot > s->d || t->rot % 8 != 0 || t->n_pos < 1 || !aligned(t->cos_sin, 16)))
     return LYCHEE_ERR_INVALID_ARG;
   if (!aligned(t->cu_new, 4) || !aligned(seqlens, 4) || !aligned(device_error, 4)) return LYCHEE_ERR_INVALID_ARG;
+  if (t->q) {
+    // rotated queries take the queries' own place or another one
+    auto span = [&](int64_t stride, int heads) {
+      return t->T > 0 ? ((size_t)(t->T - 1) * stride + (size_t)heads * s->d) * es : 0;
+    };
+    const size_t out_bytes = (size_t)t->T * s->Hq * s->d * es;
+    const bool in_place = t->q_out == t->q && (t->T <= 1 || t->q_stride == (int64_t)s->Hq * s->d);
+    if ((!in_place && overlap(t->q_out, out_bytes, t->q, span(t->q_stride, s->Hq))) ||
+        overlap(t->q_out, out_bytes, t->k, span(t->k_stride, s->Hkv)) ||
+        overlap(t->q_out, out_bytes, t->v, span(t->v_stride, s->Hkv)))
+      return LYCHEE_ERR_INVALID_ARG;
+  }
   Q8AppendParams p{};
   p.c = cache_of(s, cache);
   p.k_new = t->k;
@@ -202,6 +219,7 @@ lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const void* q, con
   const Q8Layout L = q8_layout(s, 0);
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
     return LYCHEE_ERR_WORKSPACE;
+  if (overlap(q, rows_bytes(s), out, rows_bytes(s))) return LYCHEE_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return LYCHEE_ERR_CUDA;
   Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);
@@ -231,6 +249,10 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
     return LYCHEE_ERR_INVALID_ARG;
   const Q8Layout L = q8_layout(s, k);
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return LYCHEE_ERR_WORKSPACE;
+  const size_t sets_bytes = (size_t)s->B * s->Hq * k * sizeof(int32_t);
+  if (overlap(q, rows_bytes(s), out, rows_bytes(s)) ||
+      (idx_in != idx_out && overlap(idx_in, sets_bytes, idx_out, sets_bytes)))
+    return LYCHEE_ERR_INVALID_ARG;
   const int sms = num_sms_current();
   if (sms <= 0) return LYCHEE_ERR_CUDA;
   Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);

@@ -470,7 +470,8 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
     every position's rot / 2 angles (None: no rotation); interleaved: pairs (2i, 2i + 1) instead of
     (i, i + rot / 2).  Rows of k_new, v_new and q may be parts of one projection output.
     device_error [1] int32 (or None): error bits are OR-ed into it (1 bad page, 2 bad length, 16 a
-    value that is not finite).  Returns the rotated queries [T, Hq, d], or None without q."""
+    value that is not finite).  q_out may be q itself (contiguous).  Returns the rotated queries
+    [T, Hq, d], or None without q."""
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be a tensor [T, Hkv, d]")
     shape, dt, dev = k_new.shape, k_new.dtype, k_new.device
@@ -556,7 +557,8 @@ def decode_attn_q8(q, cache, block_table, seqlens, *, out=None, workspace=None, 
     """Attention of one query token a sequence over every position of the 8-bit paged cache.
     q [B, Hq, d] (bf16 or fp32), block_table [B, max_pages] int32, seqlens [B] int32.
     workspace: uint8, q8_workspace_size(...) bytes (calls that share one must be ordered on one
-    stream; None: a fresh one).  device_error as in append_rope_q8.  Returns out [B, Hq, d]."""
+    stream; None: a fresh one).  device_error as in append_rope_q8.  out must not overlap q.
+    Returns out [B, Hq, d]."""
     sh, ptrs, _, _, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,
                                                                workspace, device_error, 0, stream)
     _q8_launch("lychee_decode_attn_q8", N.load().lychee_decode_attn_q8, dev, index, stream,
@@ -570,7 +572,7 @@ def hybrid_decode_attn_q8(q, cache, block_table, seqlens, head_role, idx_in, k, 
                           block=0):
     """hybrid_decode_attn over the 8-bit paged cache: one hybrid-head layer.  q, head_role, idx_in,
     k, k_per_seq and block as there; cache, block_table, seqlens, workspace (q8_workspace_size(...,
-    k) bytes) and device_error as in decode_attn_q8.
+    k) bytes), device_error and out as in decode_attn_q8; idx_out may be idx_in.
     Returns (out [B, Hq, d], idx_out [B, Hq, k])."""
     k = int(k)
     sh, ptrs, B, Hq, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,

@@ -393,7 +393,8 @@ typedef struct {
  *              infinity as the largest value (neither sets the scale); both set
  *              bit 16 of *device_error
  *   q_out      rotated queries, rounded to dtype; rows of tokens that no sequence
- *              owns (from cu_new[B] to T) are left as they are
+ *              owns (from cu_new[B] to T) are left as they are.  It may be q itself
+ *              (contiguous), and overlaps q, k and v in no other way
  * seqlens device [B].  A sequence whose numbers do not fit (m_b > n_b, n_b beyond
  * max_pages * page, or beyond n_pos when there is a rotation) is skipped and
  * flagged.  A page that takes new rows must belong to one sequence alone. */
@@ -408,7 +409,7 @@ LYCHEE_API size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k);
 
 /* Attention of one query token a sequence over every cached position:
  * out[b, h] = softmax(q . K_g^T / sqrt(d)) V_g over positions j < seqlens[b].
- *   q, out    device [B, Hq, d] dtype, 16-byte aligned
+ *   q, out    device [B, Hq, d] dtype, 16-byte aligned; they must not overlap
  *   workspace device, >= lychee_q8_workspace_size(s, 0) bytes, 256-byte aligned
  * Scores are exact products of the codes with q (bf16, down to 2^-27 of its largest
  * element), or with q held in two 11-bit parts (fp32), summed in fp32; softmax and
@@ -429,7 +430,8 @@ LYCHEE_API lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const v
  *   k_per_seq, head_role, idx_in, idx_out as in lychee_hybrid_decode_attn; a sparse
  *              head reads its entries before the first -1 (strictly ascending, below
  *              n_b; one that is not is flagged, and what the head then returns is
- *              unspecified).  An empty set gives zeros.
+ *              unspecified).  An empty set gives zeros.  idx_out may be idx_in, and
+ *              overlaps it in no other way.
  *   workspace  device, >= lychee_q8_workspace_size(s, k) bytes, 256-byte aligned */
 LYCHEE_API lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, int32_t block,
                                                const void* q, const lychee_q8_cache* cache,
