@@ -46,7 +46,7 @@ struct Q8AttnParams {
   const void* q;             // [B, Hq, D]
   void* out;                 // [B, Hq, D]
   const int32_t* seqlens;    // [B]
-  uint32_t* err;             // or null
+  uint32_t* err;             // the caller's word, or the workspace's
   float* parts;              // [CTAs, 2, G * (D + 2)]: states a CTA left open: of a segment that
                              // began before it, of one that began in it; m[G], l[G], acc[G][D]
   int32_t* part_seg;         // [CTAs, 2]: their segments (sequence * Hkv + KV head), -1: none

@@ -65,7 +65,8 @@ size_t rows_bytes(const lychee_q8_shape* s) {
   return (size_t)s->B * s->Hq * s->d * (s->dtype == LYCHEE_BF16 ? 2 : 4);
 }
 
-// Workspace: the states that the attention CTAs leave open; for the hybrid step
+// Workspace: the header with the error word; the states that the attention CTAs
+// leave open; for the hybrid step
 // (k > 0) also the retrieval heads' logits and the sparse heads' sets as bitmaps
 // and row lists.
 struct Q8Layout {
@@ -75,7 +76,9 @@ struct Q8Layout {
 Q8Layout q8_layout(const lychee_q8_shape* s, int k) {
   Q8Layout L{};
   const size_t state = (size_t)(s->Hq / s->Hkv) * (s->d + 2) * 4;
-  size_t at = align256(kQ8MaxCtas * 2 * sizeof(int32_t));
+  size_t at = sizeof(WsHeader);
+  L.part_seg = at;
+  at += align256(kQ8MaxCtas * 2 * sizeof(int32_t));
   L.parts = at;
   at += align256(kQ8MaxCtas * 2 * state);
   L.scratch = at;
@@ -138,7 +141,7 @@ Q8AttnParams attn_params(const lychee_q8_shape* s, const void* q, const lychee_q
   p.q = q;
   p.out = out;
   p.seqlens = seqlens;
-  p.err = err;
+  p.err = err ? err : &reinterpret_cast<WsHeader*>(ws)->err;
   p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv;
   p.N_max = n_max_of(s);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s->d));

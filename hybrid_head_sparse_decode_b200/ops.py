@@ -355,8 +355,11 @@ def q8_workspace_size(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k=
 
 def alloc_q8_workspace(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k=0,
                        device=None) -> torch.Tensor:
+    """A workspace of that size, its error word (check_device_error) zero."""
     n = q8_workspace_size(B, Hq, Hkv, d, page, num_pages, max_pages, dtype, code, k)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:4].zero_()
+    return ws
 
 
 # The calls below run once a layer and token, so what they do on the host counts: a
@@ -469,8 +472,8 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
     seqlens [B] int32 counts the new tokens.  cos_sin [n_pos, rot] fp32: cosines, then sines, of
     every position's rot / 2 angles (None: no rotation); interleaved: pairs (2i, 2i + 1) instead of
     (i, i + rot / 2).  Rows of k_new, v_new and q may be parts of one projection output.
-    device_error [1] int32 (or None): error bits are OR-ed into it (1 bad page, 2 bad length, 16 a
-    value that is not finite).  q_out may be q itself (contiguous).  Returns the rotated queries
+    device_error [1] int32: error bits are OR-ed into it (1 bad page, 2 bad length, 16 a value that is
+    not finite; None: nothing tells of them).  q_out may be q itself (contiguous).  Returns the rotated queries
     [T, Hq, d], or None without q."""
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be a tensor [T, Hkv, d]")
@@ -557,8 +560,9 @@ def decode_attn_q8(q, cache, block_table, seqlens, *, out=None, workspace=None, 
     """Attention of one query token a sequence over every position of the 8-bit paged cache.
     q [B, Hq, d] (bf16 or fp32), block_table [B, max_pages] int32, seqlens [B] int32.
     workspace: uint8, q8_workspace_size(...) bytes (calls that share one must be ordered on one
-    stream; None: a fresh one).  device_error as in append_rope_q8.  out must not overlap q.
-    Returns out [B, Hq, d]."""
+    stream; None: a fresh one).  device_error as in append_rope_q8; without it the bits go to the
+    workspace (check_device_error reads and clears them; one of alloc_q8_workspace begins with none).
+    out must not overlap q.  Returns out [B, Hq, d]."""
     sh, ptrs, _, _, dev, index, out, workspace, err = _q8_call(q, cache, block_table, seqlens, out,
                                                                workspace, device_error, 0, stream)
     _q8_launch("lychee_decode_attn_q8", N.load().lychee_decode_attn_q8, dev, index, stream,

@@ -330,7 +330,10 @@ LYCHEE_API lychee_status lychee_hardkuma_roles(const double* alpha, const double
  *     lychee_check_device_error: 1 = bad page number or bad incoming index, 2 =
  *     bad sequence length; 16 = the append met a value that is not finite).  It
  *     is never cleared here: the caller sets it to zero and reads it when it
- *     likes.
+ *     likes.  With NULL the attention calls OR them into the first word of their
+ *     workspace, which lychee_check_device_error reads and clears: the caller sets
+ *     it to zero once, and bits then stay over calls until they are read.  The
+ *     append has no workspace: with NULL it reports nothing.
  *   - A page number outside [0, num_pages) is flagged and its rows are skipped:
  *     no head attends to them, and in the sets that retrieval heads hand on they
  *     rank last (by lower position), behind every row that there is.

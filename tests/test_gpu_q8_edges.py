@@ -141,3 +141,47 @@ def test_scores_near_the_end_of_fp32(dtype, n):
     cache[2].fill_(2.0 ** 60)
     q.fill_(2.0 ** 127)
     check()
+
+
+# ---- errors without an error word of the caller's --------------------------------------------------
+
+def test_flags_go_to_the_workspace():
+    """Without device_error the bits are OR-ed into the workspace's first word, stay there over calls, and
+    check_device_error reads and clears them; with it the workspace keeps none."""
+    g = torch.Generator().manual_seed(37)
+    lens, Hq, Hkv, d, page, k = [2000, 70], 8, 2, 64, 16, 30
+    table, P = R.make_table(g, lens, page)
+    cache = to_dev(R.make_cache(g, P, Hkv, page, d, I8))
+    bad = table.clone()
+    bad[0, 3] = P
+    table, bad, seq = table.to(DEV), bad.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = torch.randn(2, Hq, d, generator=g).to(BF).to(DEV)
+    idx = torch.arange(k, dtype=torch.int32, device=DEV).expand(2, Hq, k).contiguous()
+    wrong = idx.clone()
+    wrong[1, 7, 5] = 4
+    roles = [1] + [0] * 7
+    shape = (2, Hq, Hkv, d, page, P, table.shape[1], BF, I8)
+    ws, wh = ops.alloc_q8_workspace(*shape), ops.alloc_q8_workspace(*shape, k)
+
+    def dense(table, **kw):
+        return ops.decode_attn_q8(q, cache, table, seq, workspace=ws, **kw)
+
+    def hybrid(table, sets, **kw):
+        return ops.hybrid_decode_attn_q8(q, cache, table, seq, roles, sets, k, workspace=wh, **kw)
+
+    clean, layer = dense(table), hybrid(table, idx)
+    assert ops.check_device_error(ws) == (N.OK, 0) and ops.check_device_error(wh) == (N.OK, 0)
+    dense(bad)
+    dense(table)
+    hybrid(table, wrong)
+    hybrid(table, idx, k_per_seq=torch.zeros(2, dtype=torch.int32, device=DEV))
+    assert ops.check_device_error(ws) == (N.ERR_BAD_INDEX, 1) and ops.check_device_error(wh) == (N.ERR_BAD_INDEX, 5)
+    assert ops.check_device_error(ws) == (N.OK, 0) and ops.check_device_error(wh) == (N.OK, 0)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dense(bad, device_error=err)
+    hybrid(table, wrong, device_error=err)
+    assert int(err.item()) == 1
+    assert ops.check_device_error(ws) == (N.OK, 0) and ops.check_device_error(wh) == (N.OK, 0)
+    # reading and clearing the word changes no call's results
+    again = hybrid(table, idx)
+    assert torch.equal(dense(table), clean) and torch.equal(again[0], layer[0]) and torch.equal(again[1], layer[1])
