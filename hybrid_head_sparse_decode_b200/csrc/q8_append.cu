@@ -143,12 +143,13 @@ __device__ __forceinline__ void turn_pairs(float (&x)[W], float (&y)[W], const f
 }
 
 // The new tokens of sequence b: [t0, t0 + m) at positions first ...  m = 0 when it
-// has none; a sequence whose numbers do not fit is skipped and flagged.
+// has none; a sequence whose numbers do not fit is skipped (its `lost` tokens then
+// have no position) and flagged.
 struct NewRows {
-  int t0, m, first;
+  int t0, m, first, lost;
 };
 __device__ __forceinline__ NewRows new_rows(const Q8AppendParams& p, int b, bool flag) {
-  NewRows r{b, 1, 0};
+  NewRows r{b, 1, 0, 0};
   const int n = p.seqlens[b];
   bool ok = true;
   if (p.cu_new) {
@@ -162,7 +163,10 @@ __device__ __forceinline__ NewRows new_rows(const Q8AppendParams& p, int b, bool
   if (r.m > 0) {
     const long long cap = (long long)p.c.max_pages << p.c.page_log2;
     ok = n >= r.m && n <= cap && (!p.cos_sin || n <= p.n_pos);
-    if (!ok) r.m = 0;
+    if (!ok) {
+      r.lost = r.m;
+      r.m = 0;
+    }
   }
   if (!ok && flag) flag_error(p.err, kErrBadSeqlen);
   r.first = n - r.m;
@@ -182,7 +186,7 @@ __device__ __forceinline__ int find_block(const Q8AppendParams& p, int blk, bool
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (p.B <= 32) {
     // every warp by itself
-    NewRows r{0, 0, 0};
+    NewRows r{0, 0, 0, 0};
     if (lane < p.B) r = new_rows(p, lane, flag && warp == 0);
     const int first = r.first >> p.c.page_log2;
     const int nb = r.m > 0 ? ((r.first + r.m - 1) >> p.c.page_log2) - first + 1 : 0;
@@ -206,7 +210,7 @@ __device__ __forceinline__ int find_block(const Q8AppendParams& p, int blk, bool
   int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    NewRows r{0, 0, 0};
+    NewRows r{0, 0, 0, 0};
     if (b < p.B) r = new_rows(p, b, flag);
     const int nb = r.m > 0 ? ((r.first + r.m - 1) >> p.c.page_log2) - (r.first >> p.c.page_log2) + 1 : 0;
     int incl = nb;
@@ -249,7 +253,7 @@ __device__ __forceinline__ void append_block(const Q8AppendParams& p, int item) 
   const int g = u >> 1;
   const bool is_v = u & 1;
   int j = 0;
-  NewRows rows{0, 0, 0};
+  NewRows rows{0, 0, 0, 0};
   const int b = find_block(p, blk, u == 0 && (!p.cu_new || blk == 0), j, rows);
   if (b < 0) return;
   const int page_len = 1 << p.c.page_log2, base = j << p.c.page_log2;
@@ -375,10 +379,21 @@ __device__ __forceinline__ void rotate_q(const Q8AppendParams& p, int cta, int p
     }
   }
   const NewRows rows = new_rows(p, b, false);
-  if (t < rows.t0 || t >= rows.t0 + rows.m) return;   // behind the last sequence, or skipped
+  if (t < rows.t0 || t >= rows.t0 + rows.m + rows.lost) return;   // behind the last sequence
   const LaneDims ld = lane_dims<W>(l, p.cos_sin ? p.rot : 0, p.interleaved != 0);
   const T* src = static_cast<const T*>(p.q) + (size_t)t * p.q_stride;
   T* dst = static_cast<T*>(p.q_out) + (size_t)t * p.Hq * D;
+  if (rows.lost > 0) {
+    // no position, no rotated query
+    float x[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = NAN;
+    for (int h = part * per + lane / LPR; h < h_end; h += RPW) {
+      store_row<W>(dst + h * D + ld.a, x);
+      store_row<W>(dst + h * D + ld.b, x);
+    }
+    return;
+  }
   float c[W], s[W];
   if (ld.turn) load_angles<W>(p, rows.first + t - rows.t0, l, c, s);
   for (int h0 = part * per + lane / LPR; h0 < h_end; h0 += U * RPW) {

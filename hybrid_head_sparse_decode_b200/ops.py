@@ -473,7 +473,8 @@ def append_rope_q8(k_new, v_new, cache, block_table, seqlens, cos_sin=None, *, q
     every position's rot / 2 angles (None: no rotation); interleaved: pairs (2i, 2i + 1) instead of
     (i, i + rot / 2).  Rows of k_new, v_new and q may be parts of one projection output.
     device_error [1] int32: error bits are OR-ed into it (1 bad page, 2 bad length, 16 a value that is
-    not finite; None: nothing tells of them).  q_out may be q itself (contiguous).  Returns the rotated queries
+    not finite; None: nothing tells of them, but the rotated queries of a sequence whose numbers do
+    not fit are NaN).  q_out may be q itself (contiguous).  Returns the rotated queries
     [T, Hq, d], or None without q."""
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be a tensor [T, Hkv, d]")

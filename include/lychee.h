@@ -396,7 +396,8 @@ typedef struct {
  *              infinity as the largest value (neither sets the scale); both set
  *              bit 16 of *device_error
  *   q_out      rotated queries, rounded to dtype; rows of tokens that no sequence
- *              owns (from cu_new[B] to T) are left as they are.  It may be q itself
+ *              owns (from cu_new[B] to T) are left as they are, those of a
+ *              sequence that is skipped become NaN.  It may be q itself
  *              (contiguous), and overlaps q, k and v in no other way
  * seqlens device [B].  A sequence whose numbers do not fit (m_b > n_b, n_b beyond
  * max_pages * page, or beyond n_pos when there is a rotation) is skipped and

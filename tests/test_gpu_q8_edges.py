@@ -185,3 +185,42 @@ def test_flags_go_to_the_workspace():
     # reading and clearing the word changes no call's results
     again = hybrid(table, idx)
     assert torch.equal(dense(table), clean) and torch.equal(again[0], layer[0]) and torch.equal(again[1], layer[1])
+
+
+@pytest.mark.parametrize("dtype,Hq,d,interleaved", [(BF, 8, 128, False), (F32, 16, 64, True), (BF, 2, 64, True)])
+def test_queries_of_skipped_sequences(dtype, Hq, d, interleaved):
+    """Rotated queries of a sequence whose numbers do not fit are NaN, not what the buffer held; rows of tokens that no
+    sequence owns, and of empty places, stay as they were."""
+    g = torch.Generator().manual_seed(43)
+    Hkv, page, new = 2, 16, [3, 5, 0, 40, 2, 1]
+    T = sum(new) + 2
+    table = torch.arange(12, dtype=torch.int32).view(6, 2)
+    #                  fits, beyond max_pages, none, beyond cos_sin, shorter than its new tokens, fits
+    seq = torch.tensor([20, 33, 99, 32, 1, 31], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0] + new).cumsum(0).int()
+    a = torch.rand(31, d // 2, generator=g)
+    cs = torch.cat([a.cos(), a.sin()], 1).to(DEV)
+    q, kn = torch.randn(T, Hq, d, generator=g).to(dtype).to(DEV), torch.randn(T, Hkv, d, generator=g).to(dtype).to(DEV)
+    cache = to_dev(R.make_cache(g, 12, Hkv, page, d, I8))
+    before = [t.clone() for t in cache]
+    out = torch.full_like(q, 7.0)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ops.append_rope_q8(kn, kn, cache, table.to(DEV), seq, cs, q=q, q_out=out, cu_new=cu.to(DEV), interleaved=interleaved,
+                       device_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 2
+    lost = torch.zeros(T, dtype=torch.bool, device=DEV)
+    lost[cu[1]:cu[2]] = lost[cu[3]:cu[4]] = lost[cu[4]:cu[5]] = True
+    assert bool(out[lost].isnan().all()) and not bool(out[~lost].isnan().any())
+    assert bool((out[T - 2:] == 7.0).all()) and not bool((out[:T - 2][~lost[:T - 2]] == 7.0).any())
+    for t, was in zip(cache, before):
+        assert torch.equal(t.view(torch.uint8)[2:4], was.view(torch.uint8)[2:4])
+        assert torch.equal(t.view(torch.uint8)[4:10], was.view(torch.uint8)[4:10])
+    # a token each: an empty place, a length that does not fit, below zero
+    for n, is_nan in ((0, False), (32, True), (-4, True)):
+        out = torch.full_like(q[:2], 7.0)
+        ops.append_rope_q8(kn[:2], kn[:2], cache, table[:2].contiguous().to(DEV), torch.tensor([n, 9], dtype=torch.int32, device=DEV),
+                           cs, q=q[:2], q_out=out, interleaved=interleaved)
+        torch.cuda.synchronize()
+        assert bool(out[0].isnan().all()) if is_nan else bool((out[0] == 7.0).all())
+        assert not bool(out[1].isnan().any())
