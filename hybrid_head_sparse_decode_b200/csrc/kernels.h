@@ -109,6 +109,8 @@ cudaError_t launch_combine(const CombineParams& p, int dtype, int D, cudaStream_
 // (topk.cu); just the combine when p.nheads is 0, just the top-k when cp.B is 0.
 cudaError_t launch_topk_combine(const TopkParams& p, const CombineParams& cp, int dtype, int D,
                                 cudaStream_t st);
+// Whether rows of p.N_max logits fit the top-k alone (p.alone) of B * nheads heads.
+bool topk_alone_fits(const TopkParams& p, int dtype, int D, cudaStream_t st);
 
 // Incoming index sets -> membership bitmaps, with validation; the rows are also
 // copied to idx_out (sparse heads pass their set on unchanged) (sets.cu).

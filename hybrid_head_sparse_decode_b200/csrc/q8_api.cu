@@ -246,6 +246,16 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   if ((st = check_sets(s, k, block)) != LYCHEE_OK) return st;
   int ns = 0;
   if ((st = check_roles(head_role, s->Hq, &ns)) != LYCHEE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int sms = num_sms_current();
+  TopkParams tp{};
+  tp.B = s->B; tp.Hq = s->Hq; tp.N_max = n_max_of(s); tp.k = k;
+  tp.sms = sms;
+  tp.empty_ok = 1;
+  tp.alone = 1;
+  for (int h = 0; h < s->Hq; ++h)
+    if (head_role[h] == LYCHEE_ROLE_RETRIEVAL) tp.heads[tp.nheads++] = (uint8_t)h;
+  if (ns < s->Hq && block <= 1 && !topk_alone_fits(tp, s->dtype, s->d, cs)) return LYCHEE_ERR_UNSUPPORTED;
   if (!q || !seqlens || !out || !idx_out || (ns > 0 && !idx_in)) return LYCHEE_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seqlens, 4) || !aligned(k_per_seq, 4) ||
       !aligned(idx_in, 4) || !aligned(idx_out, 4) || !aligned(device_error, 4))
@@ -256,7 +266,6 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   if (overlap(q, rows_bytes(s), out, rows_bytes(s)) ||
       (idx_in != idx_out && overlap(idx_in, sets_bytes, idx_out, sets_bytes)))
     return LYCHEE_ERR_INVALID_ARG;
-  const int sms = num_sms_current();
   if (sms <= 0) return LYCHEE_ERR_CUDA;
   Q8AttnParams p = attn_params(s, q, cache, seqlens, out, device_error, L, workspace);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -274,7 +283,6 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
   p.n_sparse = ns;
   fill_roles(p.role, head_role, s->Hq);
   if (!encode_rows(&p.tmk, cache->k, s) || !encode_rows(&p.tmv, cache->v, s)) return LYCHEE_ERR_CUDA;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (timed(kKindBuildBits, cs, [&] { return launch_q8_sets(p, s->dtype, s->d, cs); }) != cudaSuccess)
     return LYCHEE_ERR_CUDA;
   if (timed(kKindAttn, cs, [&] { return launch_q8_attn(p, s->dtype, s->code, s->d, sms, cs); }) != cudaSuccess)
@@ -285,18 +293,12 @@ lychee_status lychee_hybrid_decode_attn_q8(const lychee_q8_shape* s, int32_t k, 
     return LYCHEE_ERR_CUDA;
   if (ns == s->Hq) return LYCHEE_OK;
   // the retrieval heads' selection, as over any cache
-  TopkParams tp{};
   tp.logits = p.logits;
   tp.seqlens = seqlens;
   tp.k_per_seq = k_per_seq;
   tp.idx_out = idx_out;
   tp.err = p.err;
-  tp.B = s->B; tp.Hq = s->Hq; tp.N_max = p.N_max; tp.nwords = L.nwords; tp.k = k;
-  tp.sms = sms;
-  tp.empty_ok = 1;
-  tp.alone = 1;
-  for (int h = 0; h < s->Hq; ++h)
-    if (head_role[h] == LYCHEE_ROLE_RETRIEVAL) tp.heads[tp.nheads++] = (uint8_t)h;
+  tp.nwords = L.nwords;
   CombineParams none{};   // B = 0: selection only
   cudaError_t e;
   if (block > 1) {

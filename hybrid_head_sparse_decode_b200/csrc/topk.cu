@@ -467,6 +467,15 @@ cudaError_t launch_tc(const TopkParams& p, const CombineParams& cp, cudaStream_t
   return cudaGetLastError();
 }
 
+// (See launch_tc_d.)
+template <typename T, int D>
+bool takes16(const TopkParams& p, cudaStream_t st) {
+  const long long ctas16 = 16LL * p.B * p.nheads;
+  const bool one_wave = p.sms <= 0 || ctas16 <= 2LL * p.sms;
+  const bool long_rows = p.N_max > 32768;
+  return long_rows && one_wave && cluster16_ok<T, D>(p.N_max, st);
+}
+
 template <typename T, int D>
 cudaError_t launch_tc_d(const TopkParams& p, const CombineParams& cp, cudaStream_t st) {
   // With the combine in the same launch (a single layer, a stack's last layer):
@@ -479,15 +488,17 @@ cudaError_t launch_tc_d(const TopkParams& p, const CombineParams& cp, cudaStream
   // SMs at once where one of 16 needs 8 (measured: the 36-layer 128K step is
   // about 50 us shorter).
   if (cp.B == 0 && !p.alone) return launch_tc<8, T, D>(p, cp, st);
-  const long long ctas16 = 16LL * p.B * p.nheads;
-  const bool one_wave = p.sms <= 0 || ctas16 <= 2LL * p.sms;
-  const bool long_rows = p.N_max > 32768;
-  return long_rows && one_wave && cluster16_ok<T, D>(p.N_max, st)
-             ? launch_tc<16, T, D>(p, cp, st)
-             : launch_tc<8, T, D>(p, cp, st);
+  return takes16<T, D>(p, st) ? launch_tc<16, T, D>(p, cp, st) : launch_tc<8, T, D>(p, cp, st);
 }
 
 }  // namespace
+
+bool topk_alone_fits(const TopkParams& p, int dtype, int D, cudaStream_t st) {
+  if (Geometry<8>(p.N_max).ok) return true;
+  if (!Geometry<16>(p.N_max).ok) return false;
+  if (dtype == 0) return D == 128 ? takes16<__nv_bfloat16, 128>(p, st) : takes16<__nv_bfloat16, 64>(p, st);
+  return D == 128 ? takes16<float, 128>(p, st) : takes16<float, 64>(p, st);
+}
 
 cudaError_t launch_topk_combine(const TopkParams& p, const CombineParams& cp, int dtype, int D,
                                 cudaStream_t st) {

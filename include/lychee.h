@@ -431,6 +431,9 @@ LYCHEE_API lychee_status lychee_decode_attn_q8(const lychee_q8_shape* s, const v
  * positions), sparse heads attend to their incoming set and hand it on.
  *   k          capacity of an index row, 1 .. max_pages * page
  *   block      as lychee_shape.block
+ * With retrieval heads the table's capacity, max_pages * page, is at most
+ * 5 094 400 positions, or 8 091 648 while B times the retrieval heads is at most
+ * SMs / 8, or with blocks 32768 of them: LYCHEE_ERR_UNSUPPORTED above.
  *   k_per_seq, head_role, idx_in, idx_out as in lychee_hybrid_decode_attn; a sparse
  *              head reads its entries before the first -1 (strictly ascending, below
  *              n_b; one that is not is flagged, and what the head then returns is
