@@ -112,29 +112,6 @@ bool tma_gathers_disabled() {
   return off;
 }
 
-// Failure-path testing of the attention kernel's bounded waits, read once from
-// the environment: LYCHEE_TEST_WAIT_LIMIT_MS=<ms> shortens the limit after
-// which its pipeline waits give up (default 2 s), and
-// LYCHEE_TEST_WITHHOLD_ITEM=1 makes every CTA's builder withhold the
-// announcement of its first work item, so that the waits on that item run out:
-// the call then reports LYCHEE_ERR_TIMEOUT through lychee_check_device_error
-// and every kernel returns.  Neither is meant for use outside tests.
-uint64_t attn_wait_limit_ns() {
-  static const uint64_t ns = [] {
-    const char* v = std::getenv("LYCHEE_TEST_WAIT_LIMIT_MS");
-    const long ms = v ? std::strtol(v, nullptr, 10) : 0;
-    return ms > 0 ? (uint64_t)ms * 1000000ull : kWaitLimitNs;
-  }();
-  return ns;
-}
-bool attn_withhold_first_item() {
-  static const bool on = [] {
-    const char* v = std::getenv("LYCHEE_TEST_WITHHOLD_ITEM");
-    return v && v[0] == '1';
-  }();
-  return on;
-}
-
 // The cache [B, Hkv, N_max, d] as rows of d elements, box one row high and one
 // row wide (the form tile::gather4 needs).  False when it cannot be described
 // (no encoder, or more rows than a 32-bit coordinate reaches); the kernel then
@@ -365,7 +342,7 @@ lychee_status run_layer(const Ctx& c, const void* q, const void* kc, const void*
     ap.t_heads = s->B * Hq;
     ap.t_win = plan.tail_win;
   }
-  ap.wait_ns = attn_wait_limit_ns();
+  ap.wait_ns = attn_wait_limit_ns(kWaitLimitNs);
   ap.withhold_first = attn_withhold_first_item() ? 1 : 0;
   if (plan.span_start) span_mark(false, c.st);
   e = timed(kKindAttn, c.st, [&] { return launch_attn(ap, s->dtype, s->d, G, c.sms, c.st); });

@@ -8,6 +8,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <cstdlib>
 #include <mutex>
 #include <vector>
 
@@ -69,6 +70,31 @@ inline int num_sms_current() {
     cache[dev] = n;
   }
   return cache[dev];
+}
+
+// ---- failure-path testing ---------------------------------------------------------
+// For the attention kernels' bounded waits, read once from
+// the environment: LYCHEE_TEST_WAIT_LIMIT_MS=<ms> shortens the limit after
+// which their pipeline waits give up (`usual`: 2 s), and
+// LYCHEE_TEST_WITHHOLD_ITEM=1 makes every CTA's builder withhold the
+// announcement of its first work item (the 8-bit cache's kernel: makes every warp's
+// first stage expect an arrival that never comes), so that the waits on it run out:
+// the call then reports LYCHEE_ERR_TIMEOUT through lychee_check_device_error
+// and every kernel returns.  Neither is meant for use outside tests.
+inline uint64_t attn_wait_limit_ns(uint64_t usual) {
+  static const uint64_t ns = [] {
+    const char* v = std::getenv("LYCHEE_TEST_WAIT_LIMIT_MS");
+    const long ms = v ? std::strtol(v, nullptr, 10) : 0;
+    return ms > 0 ? (uint64_t)ms * 1000000ull : 0;
+  }();
+  return ns ? ns : usual;
+}
+inline bool attn_withhold_first_item() {
+  static const bool on = [] {
+    const char* v = std::getenv("LYCHEE_TEST_WITHHOLD_ITEM");
+    return v && v[0] == '1';
+  }();
+  return on;
 }
 
 // ---- optional launch profiler ----------------------------------------------------

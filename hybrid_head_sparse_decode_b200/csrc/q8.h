@@ -64,6 +64,8 @@ struct Q8AttnParams {
   int32_t* idx_out;          // [B, Hq, k]: they go on as they came
   const int32_t* k_per_seq;  // [B] or null (checked here)
   int nwords, ntiles, k, n_sparse;
+  unsigned long long wait_ns;   // how long a wait for a slab may take
+  int withhold_first;        // test only: a warp's first stage expects an arrival that never comes
   int whole;                 // 1: CTA x takes segment x whole, nothing is left open
   // the cache's codes as rows of D bytes, boxes of 32 rows (pages of 16: 16 rows), swizzled by D bytes
   alignas(64) CUtensorMap tmk;

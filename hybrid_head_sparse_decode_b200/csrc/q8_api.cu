@@ -144,6 +144,8 @@ Q8AttnParams attn_params(const lychee_q8_shape* s, const void* q, const lychee_q
   p.err = err ? err : &reinterpret_cast<WsHeader*>(ws)->err;
   p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv;
   p.N_max = n_max_of(s);
+  p.wait_ns = attn_wait_limit_ns(kWaitLimitNs);
+  p.withhold_first = attn_withhold_first_item() ? 1 : 0;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s->d));
   return p;
 }

@@ -229,7 +229,8 @@ struct Warp {
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < kStages; ++i)
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * i) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * i), "r"(i == 0 && p.withhold_first ? 2 : 1)
+                     : "memory");
       fence_mbar_init();
     }
     __syncwarp();
@@ -926,10 +927,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
     uint32_t phase = 0;
     for (int i = 0; i < copied; ++i) {
       uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_AUX + warp * C::WARP_AUX + kStages * C::AUX) + si;
-      if (!mbar_wait(bar, phase, p.err)) {
+      // (the warp decides as one: a slab that lands at the very limit must not part its lanes)
+      if (!__all_sync(kFull, mbar_wait(bar, phase, p.err, p.wait_ns))) {
         // flagged, and the result is lost; what is still on its way gets as long again
         for (; i < copied; ++i) {
-          mbar_wait(bar, phase, p.err);
+          mbar_wait(bar, phase, p.err, p.wait_ns);
           if (++si == kStages) {
             si = 0;
             phase ^= 1u;
