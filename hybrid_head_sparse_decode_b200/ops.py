@@ -536,7 +536,7 @@ def _q8_call(q, cache, block_table, seqlens, out, workspace, device_error, k, st
         raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
     _need("q", q, dt, shape, dev, index)
     if out is None:
-        out = _empty_out(shape, dt, dev, stream)
+        out = torch.empty_like(q) if stream is None else _empty_out(shape, dt, dev, stream)
     else:
         _need("out", out, dt, shape, dev, index)
     sh, ptrs, B, _ = _q8_cache(cache, block_table, seqlens, shape[1], shape[2], dt, dev, index)

@@ -97,3 +97,34 @@ def test_refused_capacities_launch_nothing():
                                       workspace=torch.empty(1 << 20, dtype=torch.uint8, device=DEV))
         torch.cuda.synchronize()
         assert bool((out == 3.0).all()) and bool((nxt == 9).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page,code", [(128, E4), (16, I8)])
+def test_a_cache_of_more_than_4_gib(page, code):
+    """Codes beyond 2^32 bytes: the same bits as from a small cache, appended, attended to and selected from."""
+    g = torch.Generator().manual_seed(61)
+    Hq, Hkv, d, lens, k = 8, 2, 128, [3001, 500], 300
+    P = (4500 << 20) // (Hkv * page * d)
+    table, small_pages = R.make_table(g, lens, page)
+    small = ops.Q8Cache(*(t.to(DEV) for t in R.make_cache(g, small_pages, Hkv, page, d, code)))
+    big = ops.alloc_q8_cache(P, Hkv, page, d, code, DEV)
+    # page i of the small cache lies near the big one's end, or (every third) where it is
+    at = torch.arange(small_pages)
+    at = torch.where(at % 3 == 0, at, P - 1 - at)
+    assert big.k.numel() > 1 << 32 and int(at.max()) * Hkv * page * d > 1 << 32
+    for a, b in zip(big, small):
+        a.view(torch.uint8)[at.to(DEV)] = b.view(torch.uint8)
+    far = torch.where(table >= 0, at[table.clamp(min=0).long()].int(), -1).int()
+    seq = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q, rows = torch.randn(2, Hq, d, generator=g).to(BF).to(DEV), torch.randn(40, Hkv, d, generator=g).to(BF).to(DEV)
+    idx = torch.stack([torch.stack([torch.randperm(n, generator=g)[:k].sort().values for _ in range(Hq)]) for n in lens]).int().to(DEV)
+    cu = torch.tensor([0, 17, 40], dtype=torch.int32, device=DEV)
+    got = []
+    for c, t in ((small, table.to(DEV)), (big, far.to(DEV))):
+        ops.append_rope_q8(rows, rows, c, t, seq, cu_new=cu)
+        got.append([ops.decode_attn_q8(q, c, t, seq), *ops.hybrid_decode_attn_q8(q, c, t, seq, [1] + [0] * 7, idx, k)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    for a, b in zip(big, small):
+        assert torch.equal(a.view(torch.uint8)[at.to(DEV)], b.view(torch.uint8))
