@@ -38,8 +38,7 @@ constexpr int kQ8Warps = 12;       // warps of an attention CTA (one CTA an SM)
 constexpr int kQ8Stages = 2;       // slabs in a warp's ring
 constexpr int kQ8Slab = 32;        // rows of a slab
 constexpr int kQ8MaxCtas = 160;    // attention CTAs at most (the workspace holds that many states)
-constexpr int kQ8MinSlabs = 1;     // slabs a warp takes at least, while there are any
-constexpr int kQ8WholeMax = 1024;  // positions of a segment that one CTA takes alone, at most
+constexpr int kQ8WholeMax = 1024;  // positions of the widest table whose segments are one CTA's each
 constexpr int kQ8Tile = 4096;      // positions of a tile (hybrid: the unit whose rows are listed)
 struct Q8AttnParams {
   Q8Cache c;

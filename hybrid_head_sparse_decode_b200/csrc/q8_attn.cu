@@ -9,9 +9,8 @@
 // rounding of the cache, and take the scales afterwards.
 //
 // Numbers.  The codes become halves (exact: both code types fit 11 bits).  (The
-// 8-bit form of mma.sync with q in two parts took 490 instructions for 16 rows
-// against 415: the compiler turns it into the same conversions and twice the
-// products.)  q is scaled by a power of
+// 8-bit form of mma.sync with q in two parts: 490 executed instructions for 16 rows
+// against 415, 54 us against 52 for 131072 positions.)  q is scaled by a power of
 // two that brings its largest magnitude to [2^13, 2^14): a bf16 is then a half
 // exactly down to 2^-27 of the largest, and an fp32 is held in two halves (22
 // bits).  The weight that multiplies the values' codes is w_j = p_j sv_j; it is what
@@ -35,7 +34,7 @@
 // absent rows as zeros).  At the end the CTA merges its warps' states of a segment, writes what
 // is complete and leaves at most two states open: of a segment that began in an
 // earlier CTA and of one that goes on in a later CTA.  The second kernel merges
-// those.  When there are fewer segments than CTAs and they are short, every
+// those.  When there are fewer segments than CTAs and the table is narrow, every
 // segment is one CTA's and nothing is left to merge.  All sums have a fixed order.
 //
 // Layouts.  Rows lie in shared memory with the TMA's swizzle (16-byte pieces of a
@@ -783,10 +782,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attn_kernel(const __grid_const
   const int n_items = HYB ? p.B * p.Hkv * p.ntiles : p.B;
   Start s0{0, 0, 0};
   int mine = 0;
-  // the ranges of [0, total) units: per CTA, at least kQ8MinSlabs a warp, then per warp
+  // the ranges of [0, total) units: per CTA, at least one a warp, then per warp
   int c0 = 0, c1 = 0, per_warp = 1;
   auto cut_ranges = [&](int total) {
-    const int per_cta = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kQ8MinSlabs * kWarps);
+    const int per_cta = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kWarps);
     c0 = (int)min((long long)total, (long long)per_cta * blockIdx.x);
     c1 = (int)min((long long)total, (long long)c0 + per_cta);
     per_warp = max((c1 - c0 + kWarps - 1) / kWarps, 1);
@@ -1155,10 +1154,12 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
 
 // ---- launches ----
 int attn_grid(int sms) { return std::min(sms, kQ8MaxCtas); }
-// A segment per CTA when that leaves no segment over and none is longer than
+// A segment per CTA when that leaves no segment over and none can be longer than
 // kQ8WholeMax positions: nothing is left open, and one launch less than splitting.
-// (8 KV heads of 128, one sequence: 512 positions 7.0 us against 10.1 split, 1024 9.4
-// against 10.2, 2048 14.0 against 10.4; eight sequences of 1024: 9.8 against 12.3.)
+// The host does not see the lengths, so the rule goes by the table's capacity: short
+// sequences in a wide table are split.  (8 KV heads of 128, one sequence that fills its
+// table: 512 positions 7.0 us against 10.1 split, 1024 9.4 against 10.2, 2048 14.0 against
+// 10.4; eight sequences of 1024: 9.8 against 12.3.)
 bool takes_whole(const Q8AttnParams& p, int grid) {
   return (long long)p.B * p.Hkv <= grid && p.N_max <= kQ8WholeMax;
 }

@@ -408,7 +408,9 @@ LYCHEE_API lychee_status lychee_append_rope_q8(const lychee_q8_shape* s, const l
 
 /* Bytes of device workspace for lychee_decode_attn_q8 (k = 0) or
  * lychee_hybrid_decode_attn_q8 with index rows of capacity k.  0 if *s or k is
- * invalid. */
+ * invalid.  With k > 0 it grows with the table's capacity, whatever the lengths: about
+ * B * max_pages * page * (4 Hq + Hq / 8 + 5 Hkv) bytes (logits of every query head,
+ * sets as bits, row lists). */
 LYCHEE_API size_t lychee_q8_workspace_size(const lychee_q8_shape* s, int32_t k);
 
 /* Attention of one query token a sequence over every cached position:
