@@ -315,7 +315,8 @@ LYCHEE_API lychee_status lychee_hardkuma_roles(const double* alpha, const double
  *          page are not read.  Sequences may share pages that nothing is
  *          appended to (a common prefix).
  * Scales are powers of two 2^e, -60 <= e <= 60, as the append writes them.
- * Attention takes any positive finite scale within that range.
+ * Attention takes any positive finite scale within that range; where the V scales
+ * of one sequence lie more than 2^96 apart, weights below 2^-24 may be lost.
  * e4m3's NaN codes are no values: the append writes none, and none may stand in a
  * row that is attended to.  Rows behind a sequence's end may hold anything.
  *

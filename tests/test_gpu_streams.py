@@ -73,6 +73,30 @@ def test_what_a_call_allocates_belongs_to_its_stream(make, monkeypatch):
     torch.cuda.synchronize()
 
 
+def test_a_forked_stream_in_a_capture():
+    """A call on a stream that a capture was forked to, making its own workspace and outputs: replays give its results."""
+    calls = q8_job(7)[:2]
+    want = [[t.clone() for t in call(None)] for call in calls]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for call in calls:
+            call(side)                            # (dropped at once)
+        got = [call(side) for call in calls]
+        torch.cuda.current_stream().wait_stream(side)
+        kept = [[t.clone() for t in outs] for outs in got]
+    del got
+    for _ in range(3):
+        for outs in kept:
+            for t in outs:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for outs, ref in zip(kept, want) for a, b in zip(outs, ref))
+
+
 def test_two_streams_without_workspaces():
     """Calls side by side on two streams, each with a workspace of its own making, other work on the current stream taking
     memory meanwhile: the results of the calls alone."""

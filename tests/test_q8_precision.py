@@ -86,3 +86,22 @@ def test_attention_keeps_its_bits(case, dtype, code):
     out = ops.decode_attn_q8(q.to(DEV), ops.Q8Cache(*(t.to(DEV) for t in cache)), table.to(DEV), seq.to(DEV))
     torch.cuda.synchronize()
     assert keeps(out.cpu(), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,code", [(BF, E4), (F32, I8)])
+@pytest.mark.parametrize("case", CASES[3:], ids=str)
+def test_hybrid_layers_keep_them(case, dtype, code):
+    """The hybrid layer's ways of reading rows: consecutive ones for retrieval heads, with bits for sparse heads beside them,
+    listed ones for sparse heads alone.  (Sets of every position: the values of the attention over all.)"""
+    q, cache, table, seq = inputs(*case, dtype, code)
+    ref = attend(q, cache, table, seq)
+    B, Hq, n = q.shape[0], q.shape[1], int(seq.max())
+    idx = torch.full((B, Hq, n), -1, dtype=torch.int32)
+    for b, m in enumerate(seq.tolist()):
+        idx[b, :, :m] = torch.arange(m, dtype=torch.int32)
+    dev = ops.Q8Cache(*(t.to(DEV) for t in cache))
+    for roles in ([1] * Hq, [0] * Hq, [1] + [0] * (Hq - 1)):
+        out, _ = ops.hybrid_decode_attn_q8(q.to(DEV), dev, table.to(DEV), seq.to(DEV), roles, idx.to(DEV), n)
+        torch.cuda.synchronize()
+        assert keeps(out.cpu(), ref)
